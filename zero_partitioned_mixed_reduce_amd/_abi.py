@@ -7,7 +7,9 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "lib", "libzero_shard.so")
 
 ZERO_OK, ZERO_EINVAL, ZERO_ENOMEM, ZERO_EHIP, ZERO_ESTATE = 0, -1, -2, -3, -4
-ZERO_F16, ZERO_BF16 = 1, 2
+ZERO_F16, ZERO_BF16, ZERO_F32 = 1, 2, 3
+ZERO_NORM_L2, ZERO_NORM_MAX = 1, 2
+ZERO_CLIP_GLOBAL, ZERO_CLIP_EACH = 1, 2
 ZERO_ACCUMULATED = -1
 ZERO_DEVICE_LOSS_SCALE = 0.0
 ZERO_STATIC_WORKSPACE_BYTES = 8 * 1024 * 1024
@@ -53,6 +55,19 @@ class zero_adam_hparams_t(ctypes.Structure):
                 ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float)]
 
 
+class zero_grads_tensor_t(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("src_pitch", ctypes.c_int64), ("dst_pitch", ctypes.c_int64), ("src_dtype", ctypes.c_int32),
+                ("dst_dtype", ctypes.c_int32)]
+
+
+class zero_grads_info_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("elems", "num_chunks", "workspace_bytes")]
+
+    def as_dict(self):
+        return {n: getattr(self, n) for n, _ in self._fields_}
+
+
 _PROTOS = {
     "zero_shard_plan": [ctypes.POINTER(zero_shard_desc_t), ctypes.POINTER(zero_shard_info_t)],
     "zero_shard_init": [ctypes.POINTER(zero_shard_desc_t), ctypes.POINTER(zero_shard_bufs_t), ctypes.c_void_p,
@@ -86,6 +101,23 @@ _PROTOS = {
                          ctypes.POINTER(ctypes.c_float), ctypes.c_void_p],
     "zero_export_state": [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p],
     "zero_shard_destroy": [ctypes.c_void_p],
+    # gradient lists, include/zero_grads.h
+    "zero_grads_plan": [ctypes.POINTER(zero_grads_tensor_t), ctypes.c_int64, ctypes.POINTER(zero_grads_info_t)],
+    "zero_grads_init": [ctypes.POINTER(zero_grads_tensor_t), ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                        ctypes.c_void_p, ctypes.POINTER(ctypes.c_void_p)],
+    "zero_grads_info": [ctypes.c_void_p, ctypes.POINTER(zero_grads_info_t)],
+    "zero_grads_bind": [ctypes.c_void_p, ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_void_p),
+                        ctypes.c_void_p],
+    "zero_grads_norm": [ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_int32, ctypes.c_void_p],
+    "zero_grads_device": [ctypes.c_void_p] + [ctypes.POINTER(ctypes.c_void_p)] * 5,
+    "zero_grads_clip": [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_double, ctypes.c_float,
+                        ctypes.c_void_p],
+    "zero_grads_clip_norm": [ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_int32, ctypes.c_int32,
+                             ctypes.c_float, ctypes.c_void_p],
+    "zero_grads_scale": [ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p],
+    "zero_grads_query": [ctypes.c_void_p, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int32),
+                         ctypes.POINTER(ctypes.c_float), ctypes.c_void_p],
+    "zero_grads_destroy": [ctypes.c_void_p],
     # offloaded (host) step, include/zero_offload.h
     "zero_offload_init": [ctypes.POINTER(zero_shard_desc_t), ctypes.POINTER(zero_offload_bufs_t), ctypes.c_void_p,
                           ctypes.c_int32, ctypes.c_void_p, ctypes.POINTER(ctypes.c_void_p)],
@@ -272,6 +304,66 @@ def zero_export_state(h, which, dst_ptr, stream):
 
 def zero_shard_destroy(h):
     _call("zero_shard_destroy", h)
+
+
+def zero_grads_plan(tensors):
+    """tensors: a ctypes array of zero_grads_tensor_t."""
+    info = zero_grads_info_t()
+    _call("zero_grads_plan", tensors, len(tensors), ctypes.byref(info))
+    return info
+
+
+def zero_grads_init(tensors, workspace_ptr, workspace_capacity, stream):
+    h = ctypes.c_void_p()
+    _call("zero_grads_init", tensors, len(tensors), workspace_ptr, workspace_capacity, stream, ctypes.byref(h))
+    return h
+
+
+def zero_grads_info(h):
+    info = zero_grads_info_t()
+    _call("zero_grads_info", h, ctypes.byref(info))
+    return info
+
+
+def zero_grads_bind(h, src_ptrs, dst_ptrs, stream):
+    """src_ptrs: one address per tensor; dst_ptrs: the same, or None for a list planned in place."""
+    n = len(src_ptrs)
+    src = (ctypes.c_void_p * n)(*src_ptrs)
+    dst = (ctypes.c_void_p * n)(*dst_ptrs) if dst_ptrs is not None else None
+    _call("zero_grads_bind", h, src, dst, stream)
+
+
+def zero_grads_norm(h, norm, inv_loss_scale, per_tensor, stream):
+    _call("zero_grads_norm", h, norm, inv_loss_scale, int(bool(per_tensor)), stream)
+
+
+def zero_grads_device(h):
+    """Device addresses (ints): acc, found_inf, norm, tensor_acc, norms."""
+    p = [ctypes.c_void_p() for _ in range(5)]
+    _call("zero_grads_device", h, *[ctypes.byref(x) for x in p])
+    return [x.value for x in p]
+
+
+def zero_grads_clip(h, scope, other_ranks_found_inf, other_ranks_acc, max_norm, stream):
+    _call("zero_grads_clip", h, scope, int(bool(other_ranks_found_inf)), other_ranks_acc, max_norm, stream)
+
+
+def zero_grads_clip_norm(h, norm, inv_loss_scale, per_tensor, scope, max_norm, stream):
+    _call("zero_grads_clip_norm", h, norm, inv_loss_scale, int(bool(per_tensor)), scope, max_norm, stream)
+
+
+def zero_grads_scale(h, factor, stream):
+    _call("zero_grads_scale", h, factor, stream)
+
+
+def zero_grads_query(h, stream):
+    nrm, f, c = ctypes.c_double(), ctypes.c_int32(), ctypes.c_float()
+    _call("zero_grads_query", h, ctypes.byref(nrm), ctypes.byref(f), ctypes.byref(c), stream)
+    return dict(norm=nrm.value, found_inf=bool(f.value), coef=c.value)
+
+
+def zero_grads_destroy(h):
+    _call("zero_grads_destroy", h)
 
 
 def zero_offload_init(desc, bufs, master_init_ptr, num_threads, stream):

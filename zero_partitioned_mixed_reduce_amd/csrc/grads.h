@@ -1,0 +1,119 @@
+// Internal layout of the gradient-list operators, shared by the host plan and the kernels.
+#pragma once
+#include <stdint.h>
+
+#include <string>
+#include <vector>
+
+#include "zero_grads.h"
+
+namespace zs {
+
+// Elements of a block's work item.
+#ifndef ZS_GRADS_CHUNK
+#define ZS_GRADS_CHUNK 8192
+#endif
+constexpr int kGradsChunk = ZS_GRADS_CHUNK;
+static_assert(kGradsChunk % 8 == 0, "chunk starts keep a tensor's alignment");
+// A tensor of at most this many elements is one work item of a single wave, so that a block of
+// four waves takes four of them.
+#ifndef ZS_GRADS_SMALL
+#define ZS_GRADS_SMALL 1024
+#endif
+constexpr int kGradsSmall = ZS_GRADS_SMALL;
+constexpr int kGradsBlock = 256;
+constexpr int kGradsWaves = kGradsBlock / 64;
+// Blocks whose partial results one group combines (see grads_finish).
+constexpr int kGradsGroup = 256;
+// The launch limit (2^32 - 1 threads in a grid), for work items and, one block each, tensors.
+constexpr int64_t kGradsMaxBlocks = (1 << 24) - 1;
+
+// One work item: rows runs of cols elements.  The table holds the block items first, then the
+// wave items, each in list order.
+struct alignas(64) GradsChunk {
+  uint64_t src, dst;              // addresses of the first element
+  int64_t src_off, dst_off;       // their byte offsets in the tensor
+  int64_t src_pitch, dst_pitch;   // bytes from row to row
+  int32_t rows, cols;
+  int32_t tensor;
+  int16_t src_dtype, dst_dtype;
+};
+static_assert(sizeof(GradsChunk) == 64, "work item layout");
+
+// A tensor's work items: [first, first + count) of the table.
+struct GradsRange {
+  int32_t first, count;
+};
+
+// Device-resident results (first 256 bytes of the workspace).
+struct alignas(256) GradsScalars {
+  double acc;        // sum of squares, or the largest magnitude
+  int32_t flag;      // acc is not finite
+  uint32_t counter;  // groups that have completed (re-armed by the last)
+  float norm;        // in fp32; the one clipped by after a clip
+  float coef;        // global coefficient of the last clip
+  double clip_norm;  // global norm of the last clip
+  int32_t clip_flag;
+};
+static_assert(sizeof(GradsScalars) == 256, "scalar block");
+
+// Where a tensor's results go: a destination of its own, itself because none was given, or
+// itself as the destination given.
+enum GradsInto : uint8_t { kInto = 0, kInPlace = 1, kInPlaceGiven = 2 };
+
+struct GradsLayout {
+  int64_t chunks, ranges, tensor_acc, norms, part, wave_part, gcount, gpart, end;
+};
+
+struct GradsPlan {
+  zero_grads_info_t info;
+  std::vector<zero_grads_tensor_t> tensors;  // in-place destinations filled in, contiguous rows merged
+  std::vector<uint8_t> in_place;             // kInto, kInPlace or kInPlaceGiven
+  int64_t overlap;                           // a tensor with no destination that shares elements with another, or -1
+  std::vector<GradsChunk> chunks;
+  std::vector<GradsRange> ranges;
+  int64_t n_block_items;  // the rest are wave items
+  int64_t n_blocks;
+  int64_t max_count;      // work items of the largest tensor
+  int64_t bytes_in, bytes_out;
+  GradsLayout layout;
+};
+
+// Validates a list and sizes its work table.  ZERO_OK or ZERO_EINVAL with *err set.
+zero_status_t build_grads_plan(const zero_grads_tensor_t* t, int64_t n, GradsPlan* out, std::string* err);
+// Fills the work table of a validated plan (chunks, ranges).
+void fill_grads_chunks(GradsPlan* p);
+// Checks the addresses of a normalised list: null, misaligned or overlapping ones.  Tensors
+// without a destination may repeat and overlap while only norms are taken; *overlap receives
+// one of them, or -1.
+zero_status_t check_grads_addresses(const std::vector<zero_grads_tensor_t>& t, const std::vector<uint8_t>& in_place,
+                                    int64_t* overlap, std::string* err);
+
+inline int64_t grads_groups(int64_t n_blocks) { return (n_blocks + kGradsGroup - 1) / kGradsGroup; }
+
+// Tensors whose new addresses one launch of the bind kernel carries (kernel arguments hold 4 KiB).
+constexpr int kGradsBind = 240;
+struct GradsBindArgs {
+  GradsChunk* chunks;
+  const GradsRange* ranges;
+  int32_t first;  // index of the first tensor
+  uint64_t src[kGradsBind], dst[kGradsBind];
+};
+
+struct GradsArgs {
+  const GradsChunk* chunks;
+  int32_t n_block_items, n_chunks, n_blocks;
+  int32_t n_tensors;
+  const GradsRange* ranges;
+  GradsScalars* sc;
+  double* tensor_acc;
+  float* norms;
+  uint64_t* part;       // one per block
+  uint64_t* wave_part;  // one per wave item
+  uint32_t* gcount;     // one 64-byte line per group
+  uint64_t* gpart;      // one per group
+  int64_t max_count;
+  int64_t bytes_in, bytes_out;
+};
+
+}  // namespace zs

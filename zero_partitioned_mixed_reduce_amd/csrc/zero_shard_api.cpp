@@ -40,6 +40,7 @@ zero_status_t hip_fail(const char* what, hipError_t e) {
   } while (0)
 
 enum Phase { kReady, kReduced, kChecked, kNormed, kStepped };
+using zs::DeviceGuard;
 using zs::kGradAcc;
 using zs::kGradAccChunk16;
 using zs::kGradAccFlat16;
@@ -91,17 +92,6 @@ struct zero_shard {
 };
 
 namespace {
-
-struct DeviceGuard {
-  int prev = -1;
-  bool changed = false;
-  explicit DeviceGuard(int dev) {
-    if (hipGetDevice(&prev) == hipSuccess && prev != dev) changed = hipSetDevice(dev) == hipSuccess;
-  }
-  ~DeviceGuard() {
-    if (changed) (void)hipSetDevice(prev);
-  }
-};
 
 // Grid cap of the streaming kernels, in blocks per CU.  The default leaves the
 // grid at one block per work item (the hardware dispatcher balances the load);

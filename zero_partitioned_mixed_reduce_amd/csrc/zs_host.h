@@ -4,6 +4,7 @@
 
 #include <string>
 
+#include "grads.h"
 #include "zero_shard.h"
 #include "zs_internal.h"
 
@@ -11,6 +12,18 @@ namespace zs {
 
 // Sets the calling thread's message for zero_last_error() and returns s.
 zero_status_t set_error(zero_status_t s, const std::string& msg);
+
+// Makes `dev` the current device for the guard's lifetime.
+struct DeviceGuard {
+  int prev = -1;
+  bool changed = false;
+  explicit DeviceGuard(int dev) {
+    if (hipGetDevice(&prev) == hipSuccess && prev != dev) changed = hipSetDevice(dev) == hipSuccess;
+  }
+  ~DeviceGuard() {
+    if (changed) (void)hipSetDevice(prev);
+  }
+};
 
 }  // namespace zs
 
@@ -39,4 +52,14 @@ hipError_t launch_adam_step(int dtype, int grad_source, bool cast, const Chunk* 
                             float* v, DevScalars* sc, int32_t other_flag, double other_sumsq, bool sumsq_global,
                             float max_norm, float inv, const zero_adam_hparams_t* hp, const zero_loss_scaler_t* dyn,
                             const SegArgs* seg, int64_t grid_cap, hipStream_t st);
+}  // namespace zs
+
+// Kernel launchers of the gradient lists (grads.hip).
+namespace zs {
+hipError_t launch_grads_arm(const GradsArgs& a, hipStream_t st);
+hipError_t launch_grads_norm(const GradsArgs& a, int kind, float inv, bool per_tensor, hipStream_t st);
+hipError_t launch_grads_clip(const GradsArgs& a, int kind, int scope, float inv, int other_flag, double other_acc,
+                             float max_norm, hipStream_t st);
+hipError_t launch_grads_scale(const GradsArgs& a, float factor, hipStream_t st);
+hipError_t launch_grads_bind(const GradsBindArgs& a, int n, hipStream_t st);
 }  // namespace zs
