@@ -79,8 +79,8 @@ typedef struct {
   int64_t workspace_bytes; /* device workspace the caller allocates (256-byte aligned) */
 } zero_grads_info_t;
 
-/* Sizes only; no GPU work.  1 <= n <= 2^24 - 1 tensors, at most 2^60 elements
- * and 2^24 - 1 blocks of work (about 1.3e11 elements).
+/* Sizes only; no GPU work.  1 <= n <= 2^22 - 1 tensors, at most 2^60 elements
+ * and 2^22 - 1 blocks of work (about 3.4e10 elements).
  * A destination must be its own source exactly (same address, type and pitch:
  * in place) or share no element with any source or other destination; column
  * slices of one matrix are told apart by their pitch, rows of different pitches

@@ -254,7 +254,7 @@ def test_extremes_of_fp32():
     # 1 / norm is 4.7e-41, a subnormal fp32 number: rounding to it is off by at most half of 2^-149
     assert abs(q["coef"] - 1.0 / (q["norm"] + 1e-6)) <= 2.0 ** -150
     h.zero_grads_scale(1.0)
-    assert (h._out[0] == math.inf).all()
+    assert (h._out == math.inf).all()
     small = torch.full((3000,), 1e-40, device="cuda")                     # subnormal
     h = ZeroGrads([small])
     h.zero_grads_norm()
@@ -488,7 +488,7 @@ def test_captured(scope):
         assert h.query()["found_inf"] == (step == 3)
         a, n = out.clone(), h.norms.clone()
         check.zero_grads_clip_norm(0.01, scope=scope)
-        assert (bits(check._out[0]) == bits(a[:5000])).all() and (bits(a) == bits(torch.cat(check._out))).all()
+        assert (bits(a) == bits(check._out)).all()
         assert torch.equal(check.norms, n) if scope == EACH else True
         c2 = out2.clone()
         h2.zero_grads_clip_norm(0.02, scope=scope)

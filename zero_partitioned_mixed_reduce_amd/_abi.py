@@ -1,5 +1,6 @@
 """ctypes binding of libzero_shard.so: the C ABI declared in include/zero_shard.h,
 with the same function and struct names.  Argument marshalling only."""
+import array
 import ctypes
 import os
 
@@ -15,6 +16,7 @@ ZERO_DEVICE_LOSS_SCALE = 0.0
 ZERO_STATIC_WORKSPACE_BYTES = 8 * 1024 * 1024
 
 c_i64p = ctypes.POINTER(ctypes.c_int64)
+_voidpp = ctypes.POINTER(ctypes.c_void_p)
 
 
 class zero_shard_desc_t(ctypes.Structure):
@@ -327,10 +329,11 @@ def zero_grads_info(h):
 
 def zero_grads_bind(h, src_ptrs, dst_ptrs, stream):
     """src_ptrs: one address per tensor; dst_ptrs: the same, or None for a list planned in place."""
-    n = len(src_ptrs)
-    src = (ctypes.c_void_p * n)(*src_ptrs)
-    dst = (ctypes.c_void_p * n)(*dst_ptrs) if dst_ptrs is not None else None
-    _call("zero_grads_bind", h, src, dst, stream)
+    # an array of unsigned 64-bit integers is filled several times faster than one of c_void_p
+    src = array.array("Q", src_ptrs)
+    dst = array.array("Q", dst_ptrs) if dst_ptrs is not None else None
+    at = lambda a: ctypes.cast(a.buffer_info()[0], _voidpp) if a is not None else None
+    _call("zero_grads_bind", h, at(src), at(dst), stream)
 
 
 def zero_grads_norm(h, norm, inv_loss_scale, per_tensor, stream):

@@ -25,8 +25,9 @@ constexpr int kGradsBlock = 256;
 constexpr int kGradsWaves = kGradsBlock / 64;
 // Blocks whose partial results one group combines (see grads_finish).
 constexpr int kGradsGroup = 256;
-// The launch limit (2^32 - 1 threads in a grid), for work items and, one block each, tensors.
-constexpr int64_t kGradsMaxBlocks = (1 << 24) - 1;
+// Limit of the blocks of work (each up to four blocks of a launch, whose limit is 2^32 - 1
+// threads) and of the tensors.
+constexpr int64_t kGradsMaxBlocks = (1 << 22) - 1;
 
 // One work item: rows runs of cols elements.  The table holds the block items first, then the
 // wave items, each in list order.
@@ -62,7 +63,7 @@ static_assert(sizeof(GradsScalars) == 256, "scalar block");
 enum GradsInto : uint8_t { kInto = 0, kInPlace = 1, kInPlaceGiven = 2 };
 
 struct GradsLayout {
-  int64_t chunks, ranges, tensor_acc, norms, part, wave_part, gcount, gpart, end;
+  int64_t chunks, ranges, tensor_acc, norms, coefs, part, item_part, gcount, gpart, end;
 };
 
 struct GradsPlan {
@@ -75,7 +76,8 @@ struct GradsPlan {
   int64_t n_block_items;  // the rest are wave items
   int64_t n_blocks;
   int64_t max_count;      // work items of the largest tensor
-  int64_t bytes_in, bytes_out;
+  int64_t bytes_in;       // of the sources
+  bool all16;             // every source and destination is 16-bit
   GradsLayout layout;
 };
 
@@ -108,12 +110,14 @@ struct GradsArgs {
   GradsScalars* sc;
   double* tensor_acc;
   float* norms;
+  float* coefs;         // of the last clip by each tensor's norm
   uint64_t* part;       // one per block
-  uint64_t* wave_part;  // one per wave item
+  uint64_t* item_part;  // one per wave of each block item, then one per wave item
   uint32_t* gcount;     // one 64-byte line per group
   uint64_t* gpart;      // one per group
   int64_t max_count;
-  int64_t bytes_in, bytes_out;
+  int64_t bytes_in;     // of the sources
+  int32_t all16;        // every source and destination is 16-bit
 };
 
 }  // namespace zs

@@ -1,11 +1,16 @@
 // gfx950 kernels of the gradient-list operators.
 //
-// All of them walk the list's work table: one block per item of at most kGradsChunk
-// elements, and four small tensors per block, one per wave.  Elements go four at a time --
-// 8-byte accesses of 16-bit data, 16-byte accesses of fp32 -- with U groups per lane in
-// flight.  The side that is written is brought to its vector alignment by peeling at most 3
-// leading elements; the other side is read at whatever element alignment it has left (global
-// loads take any), so tensors that lie back to back at odd offsets need no slow path.
+// All of them walk the list's work table: one or more items of at most kGradsChunk elements
+// per block, or a part of one, and four small tensors per block, one per wave.  They are
+// bounded by memory traffic: a norm reads its list once, a clip reads it twice (the
+// coefficient is known only after the first time) and writes it once.  Lanes take 16 bytes at
+// a time of the wider side.  The side that is written is brought to its vector alignment by
+// peeling its leading elements; the other is read at whatever element alignment that leaves
+// (global loads take any), so tensors that lie back to back at odd offsets need no slow path.
+//
+// Measured (MI355X; a copy reaches 6.4 TB/s, pure reads 7.1): norm of 1.56e9 bf16 elements
+// 495 us, 6.3 TB/s; scaling them into another buffer 1012 us, 6.1 TB/s, and 4.1e8 fp32
+// elements into bf16 361 us, 6.7 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -14,6 +19,27 @@
 #include "grads.h"
 #include "zs_device.h"
 #include "zs_internal.h"
+
+// Tuning knobs (each set to the value measured fastest on MI355X):
+//   ZS_GRADS_NORM_U   groups per lane in flight in the norm kernel; 1 and 4 measured 0-2% slower
+//                     on lists beyond the Infinity Cache and 4-25% on shorter ones, 8 10% slower
+//   ZS_GRADS_PER      consecutive items per block of the norm kernel on lists of at least
+//                     ZS_GRADS_PER_MIN items (else one): 1.56e9 bf16 elements take 734 us at 1,
+//                     620 at 2, 495 at 4, 8 and 16; 1.2e8 take 70, 59, 52, 54 and 55
+//   ZS_GRADS_NT_BYTES a norm over a list of more bytes than this (the Infinity Cache) reads it
+//                     with non-temporal loads (1.6 GB of fp32 4-8% faster, bf16 3%)
+#ifndef ZS_GRADS_NORM_U
+#define ZS_GRADS_NORM_U 2
+#endif
+#ifndef ZS_GRADS_PER
+#define ZS_GRADS_PER 4
+#endif
+#ifndef ZS_GRADS_PER_MIN
+#define ZS_GRADS_PER_MIN 8192
+#endif
+#ifndef ZS_GRADS_NT_BYTES
+#define ZS_GRADS_NT_BYTES (256ll << 20)
+#endif
 
 namespace zs {
 
@@ -27,6 +53,7 @@ typedef ZS_GLOBAL char* dst_t;
 // Vectors at element alignment only.
 typedef f32x4 f32x4_u __attribute__((aligned(4)));
 typedef u32x2 u32x2_u __attribute__((aligned(2)));
+typedef u32x4 u32x4_u __attribute__((aligned(2)));
 
 template <int T>
 constexpr int kSize = T == ZERO_F32 ? 4 : 2;
@@ -36,20 +63,26 @@ __device__ __forceinline__ float load1(src_t p) {
   if constexpr (T == ZERO_F32) return *(const ZS_GLOBAL float*)p;
   else return dec16<T>(*(const ZS_GLOBAL uint16_t*)p);
 }
-// Four consecutive elements as they lie in memory.
-template <int T>
-struct Raw4 {
-  typename std::conditional<T == ZERO_F32, f32x4, u32x2>::type r;
+// G consecutive elements as they lie in memory: 16 or 8 bytes.
+template <int T, int G>
+struct Raw {
+  static_assert(G * kSize<T> == 16 || G * kSize<T> == 8, "one vector access");
+  typedef typename std::conditional<T == ZERO_F32, f32x4, typename std::conditional<G == 8, u32x4, u32x2>::type>::type V;
+  typedef typename std::conditional<
+      T == ZERO_F32, f32x4_u, typename std::conditional<G == 8, u32x4_u, u32x2_u>::type>::type VU;
+  V r;
 };
-template <int T>
-__device__ __forceinline__ Raw4<T> load4(src_t p) {
-  if constexpr (T == ZERO_F32) return {*(const ZS_GLOBAL f32x4_u*)p};
-  else return {*(const ZS_GLOBAL u32x2_u*)p};
+template <int T, int G, bool NT>
+__device__ __forceinline__ Raw<T, G> load(src_t p) {
+  typedef const ZS_GLOBAL typename Raw<T, G>::VU* ptr;
+  if constexpr (NT) return {__builtin_nontemporal_load((ptr)p)};
+  else return {*(ptr)p};
 }
-template <int T>
-__device__ __forceinline__ f32x4 decode4(Raw4<T> x) {
+// Elements 4 * i to 4 * i + 3 of a group.
+template <int T, int G>
+__device__ __forceinline__ f32x4 decode4(Raw<T, G> x, int i) {
   if constexpr (T == ZERO_F32) return x.r;
-  else return dec16x4<T>(x.r);
+  else return dec16x4<T>(u32x2{x.r[2 * i], x.r[2 * i + 1]});
 }
 // x as an fp32 value: keeps the compiler from joining the product that made it and an fp16
 // conversion into one instruction, which rounds once where the definition rounds twice.
@@ -62,44 +95,41 @@ __device__ __forceinline__ void store1(dst_t p, float x) {
   if constexpr (T == ZERO_F32) *(ZS_GLOBAL float*)p = x;
   else *(ZS_GLOBAL uint16_t*)p = (uint16_t)enc16<T>(rounded(x));
 }
+// Four results in the form in which they are stored.
 template <int T>
-__device__ __forceinline__ void store4(dst_t p, f32x4 x) {
-  if constexpr (T == ZERO_F32) {
-    *(ZS_GLOBAL f32x4*)p = x;
-  } else {
-    if constexpr (T == ZERO_F16) x = f32x4{rounded(x.x), rounded(x.y), rounded(x.z), rounded(x.w)};
-    *(ZS_GLOBAL u32x2*)p = enc16x4<T>(x);
-  }
+__device__ __forceinline__ u32x2 encode4(f32x4 x) {
+  return enc16x4<T>(f32x4{rounded(x.x), rounded(x.y), rounded(x.z), rounded(x.w)});
 }
-// Elements before p reaches the alignment of a group of four (0..3).
+// Elements before p reaches a multiple of `bytes`.
 template <int T>
-__device__ __forceinline__ int lead4(src_t p) {
-  constexpr uint32_t a = 4 * kSize<T>;
-  return (int)(((a - ((uint32_t)(uintptr_t)p & (a - 1))) & (a - 1)) / kSize<T>);
+__device__ __forceinline__ int lead(src_t p, uint32_t bytes) {
+  return (int)(((0u - (uint32_t)(uintptr_t)p) & (bytes - 1)) / kSize<T>);
 }
 
 // ---------------------------------------------------------------------------
 // walking a work item
 
-// First element of group g.  !FULL: g may lie beyond the run's ng groups, and the last one is
-// read in its place, so that the loads of a run's end stay unconditional and in flight
-// together.
-template <bool FULL>
+// First element of group g of G elements.  !FULL: g may lie beyond the run's ng groups, and the
+// last one is read in its place, so that the loads of a run's end stay unconditional and in
+// flight together.
+template <int G, bool FULL>
 __device__ __forceinline__ int64_t group_at(int head, int g, int ng) {
-  return head + 4 * (FULL || g < ng ? g : ng - 1);
+  return head + G * (FULL || g < ng ? g : ng - 1);
 }
 
-// One run of `len` elements by W lanes of which this is lane t.
+// One run of `len` elements by W lanes of which this is lane t, U groups of Op::kGroup
+// elements per lane in flight.
 template <int W, int U, class Op>
 __device__ __forceinline__ void walk_row(Op& op, int len, int t) {
-  int head = op.lead();
+  constexpr int G = Op::kGroup;
+  int head = op.head();
   if (head > len) head = len;
   if (t < head) op.one(t);
-  const int ng = (len - head) >> 2;  // whole groups; lane t takes t, t + W, ...
+  const int ng = (len - head) / G;  // whole groups; lane t takes t, t + W, ...
   int q = t;
   for (; q + (U - 1) * W < ng; q += U * W) op.template groups<U, W, true>(head, q, ng);
   if (q < ng) op.template groups<U, W, false>(head, q, ng);
-  const int done = head + 4 * ng;
+  const int done = head + G * ng;
   if (t < len - done) op.one(done + t);
 }
 
@@ -127,6 +157,18 @@ __device__ __forceinline__ void walk_item(Op& op, const GradsChunk& k, int t) {
 
 // ---------------------------------------------------------------------------
 // norms
+
+// A clip.  The coefficients are worked out once, on the device -- by the last block of the norm
+// kernel when the clip follows in the same call (now), else by a kernel of their own -- and not
+// by every block that scales: the square root and division in fp64 cost a block of 2048
+// elements more than its memory traffic (1.56e9 bf16 elements: 1308 us instead of 1001).
+struct ClipArgs {
+  int32_t now;
+  int32_t norm, scope;
+  float max_norm;
+  int32_t other_flag;
+  double other_acc;
+};
 
 // What a norm accumulates.  L2: squares in fp64, where the square of a float is exact, so
 // fma(d, d, s) rounds as s + d * d; four sums per lane keep the dependency chains short.  The
@@ -205,123 +247,176 @@ __device__ __forceinline__ typename A::V block_join(typename A::V x, typename A:
   return r;
 }
 
-template <int T, int KIND>
+template <int T, int KIND, bool NT>
 struct NormOp {
+  static constexpr int kGroup = 16 / kSize<T>;
   src_t base;
   int64_t pitch;
   float inv;
   Acc<KIND> acc;
   src_t s;
   __device__ __forceinline__ void row(int r) { s = base + r * pitch; }
-  __device__ __forceinline__ int lead() const { return lead4<T>(s); }
+  __device__ __forceinline__ int head() const { return lead<T>(s, 16); }
   __device__ __forceinline__ void one(int j) { acc.add(load1<T>(s + (int64_t)j * kSize<T>) * inv); }
   template <int U, int W, bool FULL>
-  __device__ __forceinline__ void groups(int head, int q, int ng) {
-    Raw4<T> x[U];
+  __device__ __forceinline__ void groups(int first, int q, int ng) {
+    Raw<T, kGroup> x[U];
 #pragma unroll
-    for (int k = 0; k < U; ++k) x[k] = load4<T>(s + group_at<FULL>(head, q + k * W, ng) * kSize<T>);
+    for (int k = 0; k < U; ++k) x[k] = load<T, kGroup, NT>(s + group_at<kGroup, FULL>(first, q + k * W, ng) * kSize<T>);
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      f32x4 u = decode4<T>(x[k]) * inv;
-      if (!FULL && q + k * W >= ng) u = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      acc.add4(u);
+#pragma unroll
+      for (int i = 0; i < kGroup / 4; ++i) {
+        f32x4 u = decode4(x[k], i) * inv;
+        if (!FULL && q + k * W >= ng) u = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        acc.add4(u);
+      }
     }
   }
 };
 
-template <int T, int KIND, int W, int U>
+template <int T, int KIND, bool NT, int W>
 __device__ __forceinline__ typename Acc<KIND>::V norm_typed(const GradsChunk& k, float inv, int t) {
-  NormOp<T, KIND> op{(src_t)k.src, k.src_pitch, inv, {}, (src_t)k.src};
-  walk_item<W, U>(op, k, t);
+  constexpr int U = ZS_GRADS_NORM_U;
+  NormOp<T, KIND, NT> op{(src_t)k.src, k.src_pitch, inv, {}, (src_t)k.src};
+  walk_item<W, W == 64 ? (T == ZERO_F32 ? 4 : 2) : U>(op, k, t);
   return op.acc.value();
 }
-template <int KIND, int W>
+template <int KIND, bool NT, int W>
 __device__ __forceinline__ typename Acc<KIND>::V norm_item(const GradsChunk& k, float inv, int t) {
-  constexpr int U16 = W == 64 ? 4 : 8;
-  if (k.src_dtype == ZERO_F32) return norm_typed<ZERO_F32, KIND, W, 4>(k, inv, t);
-  if (k.src_dtype == ZERO_BF16) return norm_typed<ZERO_BF16, KIND, W, U16>(k, inv, t);
-  return norm_typed<ZERO_F16, KIND, W, U16>(k, inv, t);
+  if (k.src_dtype == ZERO_F32) return norm_typed<ZERO_F32, KIND, NT, W>(k, inv, t);
+  if (k.src_dtype == ZERO_BF16) return norm_typed<ZERO_BF16, KIND, NT, W>(k, inv, t);
+  return norm_typed<ZERO_F16, KIND, NT, W>(k, inv, t);
+}
+
+__device__ __forceinline__ float coefficient(double norm, bool bad, float max_norm) {
+  if (bad || !(max_norm > 0.0f)) return 1.0f;
+  const double c = (double)max_norm / (norm + 1e-6);
+  return c < 1.0 ? (float)c : 1.0f;
+}
+
+// Records the global norm to clip by and its coefficient.
+__device__ __forceinline__ void clip_by(GradsScalars* sc, double acc, bool bad, const ClipArgs& c) {
+  const double norm = c.norm == ZERO_NORM_L2 ? sqrt(acc) : acc;
+  sc->norm = (float)norm;
+  sc->coef = c.scope == ZERO_CLIP_GLOBAL ? coefficient(norm, bad, c.max_norm) : 1.0f;
+  sc->clip_norm = norm;
+  sc->clip_flag = bad;
 }
 
 // Joins the blocks' results in an order fixed by the grid, without float atomics: a block
 // stores its own, arrives on its group's counter, and the group's last block joins the
-// group's results one per lane; the last group joins the groups'.  Counters are re-armed by
-// their last arrival.
+// group's results, a fixed set per lane; the last group joins the groups'.  Counters are
+// re-armed by their last arrival.  Only a block's first wave takes part beyond the block's
+// own sum; the others end and leave their places to the blocks that wait.
 template <int KIND>
-__device__ void grads_finish(typename Acc<KIND>::V mine, const GradsArgs& a) {
+__device__ void grads_finish(typename Acc<KIND>::V mine, const GradsArgs& a, const ClipArgs& c) {
   typedef Acc<KIND> A;
   __shared__ typename A::V lds[kGradsWaves];
-  __shared__ int is_last;
-  const typename A::V bsum = block_join<A>(mine, lds);
+  mine = wave_join<A>(mine);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = mine;
+  __syncthreads();
+  if (threadIdx.x >= 64) return;
+  typename A::V v = lds[0];
+  for (int w = 1; w < kGradsWaves; ++w) v = A::join(v, lds[w]);
+  const int lane = (int)threadIdx.x;
   const uint32_t b = blockIdx.x, nb = gridDim.x;
   const uint32_t g = b / kGradsGroup, g0 = g * kGradsGroup;
   const uint32_t gsize = nb - g0 < (uint32_t)kGradsGroup ? nb - g0 : (uint32_t)kGradsGroup;
   const uint32_t ngroups = (nb + kGradsGroup - 1) / kGradsGroup;
-  if (threadIdx.x == 0) {
-    A::store(a.part + b, bsum);
+  uint32_t prev = 0;
+  if (lane == 0) {
+    A::store(a.part + b, v);
     stores_complete();
-    const uint32_t prev =
-        __hip_atomic_fetch_add(a.gcount + 16 * g, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    is_last = prev + 1 == gsize;
+    prev = __hip_atomic_fetch_add(a.gcount + 16 * g, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-  __syncthreads();
-  if (!is_last) return;
-  typename A::V total =
-      block_join<A>(threadIdx.x < gsize ? A::load(a.part + g0 + threadIdx.x) : A::none(), lds);
-  if (threadIdx.x == 0) __hip_atomic_store(a.gcount + 16 * g, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (__shfl(prev, 0, 64) + 1 != gsize) return;
+  typename A::V r[kGradsGroup / 64];
+#pragma unroll
+  for (int k = 0; k < kGradsGroup / 64; ++k) {
+    const uint32_t i = (uint32_t)(lane + 64 * k);
+    r[k] = i < gsize ? A::load(a.part + g0 + i) : A::none();
+  }
+  v = r[0];
+#pragma unroll
+  for (int k = 1; k < kGradsGroup / 64; ++k) v = A::join(v, r[k]);
+  v = wave_join<A>(v);
+  if (lane == 0) __hip_atomic_store(a.gcount + 16 * g, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   if (ngroups > 1) {
-    if (threadIdx.x == 0) {
-      A::store(a.gpart + g, total);
+    if (lane == 0) {
+      A::store(a.gpart + g, v);
       stores_complete();
-      const uint32_t prev = __hip_atomic_fetch_add(&a.sc->counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      is_last = prev + 1 == ngroups;
+      prev = __hip_atomic_fetch_add(&a.sc->counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    __syncthreads();
-    if (!is_last) return;
-    typename A::V s = A::none();
-    for (uint32_t i = threadIdx.x; i < ngroups; i += kGradsBlock) s = A::join(s, A::load(a.gpart + i));
-    total = block_join<A>(s, lds);
-    if (threadIdx.x == 0) __hip_atomic_store(&a.sc->counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (__shfl(prev, 0, 64) + 1 != ngroups) return;
+    v = A::none();
+    for (uint32_t i = (uint32_t)lane; i < ngroups; i += 64) v = A::join(v, A::load(a.gpart + i));
+    v = wave_join<A>(v);
+    if (lane == 0) __hip_atomic_store(&a.sc->counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-  if (threadIdx.x == 0) {
-    const double acc = A::acc(total);
+  if (lane == 0) {
+    const double acc = A::acc(v);
     a.sc->acc = acc;
     a.sc->flag = !__builtin_isfinite(acc);
     a.sc->norm = (float)norm_of<KIND>(acc);
+    if (c.now) clip_by(a.sc, acc, !__builtin_isfinite(acc), c);
   }
 }
 
-template <int KIND>
-__global__ void __launch_bounds__(kGradsBlock) grads_norm_kernel(GradsArgs a, float inv) {
-  typename Acc<KIND>::V v = Acc<KIND>::none();
+// Blocks of whole items take `per_block` consecutive ones, so that what ends a block -- its sum,
+// a store, an arrival -- is paid once for them; the next item's table entry is requested
+// before the present item is streamed.  With item_part every wave also leaves its part of each
+// item's result.
+template <int KIND, bool NT>
+__global__ void __launch_bounds__(kGradsBlock, 8) grads_norm_kernel(GradsArgs a, float inv, int per_block, int n_runs,
+                                                                 uint64_t* item_part, ClipArgs clip) {
+  typedef Acc<KIND> A;
+  typename A::V v = A::none();
   const int b = (int)blockIdx.x;
-  if (b < a.n_block_items) {
-    const GradsChunk k = a.chunks[b];
-    v = norm_item<KIND, kGradsBlock>(k, inv, (int)threadIdx.x);
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  if (b < n_runs) {
+    int c = b * per_block;
+    const int end = c + per_block < a.n_block_items ? c + per_block : a.n_block_items;
+    GradsChunk k = a.chunks[c];
+    for (;;) {
+      const int next = c + 1;
+      const GradsChunk kn = a.chunks[next < end ? next : c];
+      const typename A::V x = norm_item<KIND, NT, kGradsBlock>(k, inv, (int)threadIdx.x);
+      if (item_part) {
+        const typename A::V w = wave_join<A>(x);
+        if ((threadIdx.x & 63) == 0) A::store(item_part + (int64_t)c * kGradsWaves + wave, w);
+      }
+      v = A::join(v, x);
+      if (next >= end) break;
+      k = kn;
+      c = next;
+    }
   } else {
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int i = (b - a.n_block_items) * kGradsWaves + wave;
+    const int i = (b - n_runs) * kGradsWaves + wave;
     if (i < a.n_chunks - a.n_block_items) {
       const GradsChunk k = a.chunks[a.n_block_items + i];
-      v = norm_item<KIND, 64>(k, inv, (int)threadIdx.x & 63);
-      const typename Acc<KIND>::V w = wave_join<Acc<KIND>>(v);
-      if ((threadIdx.x & 63) == 0) Acc<KIND>::store(a.wave_part + i, w);
+      v = norm_item<KIND, false, 64>(k, inv, (int)threadIdx.x & 63);
+      if (item_part) {
+        const typename A::V w = wave_join<A>(v);
+        if ((threadIdx.x & 63) == 0) A::store(item_part + (int64_t)a.n_block_items * kGradsWaves + i, w);
+      }
     }
   }
-  grads_finish<KIND>(v, a);
+  grads_finish<KIND>(v, a, clip);
 }
 
 // A list without elements: its norm is 0.
-__global__ void grads_empty_kernel(GradsScalars* sc) {
+__global__ void grads_empty_kernel(GradsScalars* sc, ClipArgs clip) {
   sc->acc = 0.0;
   sc->flag = 0;
   sc->norm = 0.0f;
+  if (clip.now) clip_by(sc, 0.0, false, clip);
 }
 
 // Each tensor's norm from its items' results, by W lanes per tensor, in an order fixed by
 // the number of items.
 template <int KIND, int W>
-__global__ void __launch_bounds__(kGradsBlock) grads_tensor_norms_kernel(GradsArgs a) {
+__global__ void __launch_bounds__(kGradsBlock) grads_tensor_norms_kernel(GradsArgs a, ClipArgs clip) {
   typedef Acc<KIND> A;
   __shared__ typename A::V lds[kGradsWaves];
   const int i = (int)blockIdx.x * (kGradsBlock / W) + (int)threadIdx.x / W;
@@ -329,22 +424,47 @@ __global__ void __launch_bounds__(kGradsBlock) grads_tensor_norms_kernel(GradsAr
   typename A::V s = A::none();
   if (i < a.n_tensors) {
     const GradsRange r = a.ranges[i];
-    const uint64_t* p = r.first < a.n_block_items ? a.part + r.first : a.wave_part + (r.first - a.n_block_items);
-    for (int c = t; c < r.count; c += W) s = A::join(s, A::load(p + c));
+    const bool blocks = r.first < a.n_block_items;
+    const int n = blocks ? r.count * kGradsWaves : r.count;
+    const uint64_t* p = a.item_part + (blocks ? (int64_t)r.first * kGradsWaves
+                                              : (int64_t)a.n_block_items * kGradsWaves + (r.first - a.n_block_items));
+    for (int c = t; c < n; c += W) s = A::join(s, A::load(p + c));
   }
   s = W == 64 ? wave_join<A>(s) : block_join<A>(s, lds);
   if (i < a.n_tensors && t == 0) {
     const double acc = A::acc(s);
     a.tensor_acc[i] = acc;
     a.norms[i] = (float)norm_of<KIND>(acc);
+    if (clip.now && clip.scope == ZERO_CLIP_EACH)
+      a.coefs[i] = coefficient(norm_of<KIND>(acc), a.sc->clip_flag != 0, clip.max_norm);
+  }
+}
+
+// The coefficients of a clip from the results on the device, as the norm call and an exchange
+// have left them, and other ranks'.
+__global__ void __launch_bounds__(kGradsBlock) grads_coefs_kernel(GradsArgs a, ClipArgs c) {
+  double acc = a.sc->acc;
+  if (c.norm == ZERO_NORM_L2) acc += c.other_acc;
+  else acc = c.other_acc > acc || __builtin_isnan(c.other_acc) ? c.other_acc : acc;
+  const bool bad = (a.sc->flag | c.other_flag) != 0 || !__builtin_isfinite(acc);
+  const int i = (int)blockIdx.x * kGradsBlock + (int)threadIdx.x;
+  if (i == 0) clip_by(a.sc, acc, bad, c);
+  if (c.scope == ZERO_CLIP_EACH && i < a.n_tensors) {
+    const double t = a.tensor_acc[i];
+    a.coefs[i] = coefficient(c.norm == ZERO_NORM_L2 ? sqrt(t) : t, bad, c.max_norm);
   }
 }
 
 // ---------------------------------------------------------------------------
 // clip and scale
 
-template <int S, int D>
+// NT (block items): loads and stores are non-temporal, as nothing reads either again here.
+// 1.2e8 fp16 elements, which the Infinity Cache holds, are clipped in 138 us with them and
+// 164 without; 4.1e8 fp32 ones in 636 and 665.
+template <int S, int D, bool NT>
 struct ScaleOp {
+  // 16-byte accesses on the wider side; between two 16-bit types on both
+  static constexpr int kGroup = S != ZERO_F32 && D != ZERO_F32 ? 8 : 4;
   src_t sbase;
   dst_t dbase;
   int64_t spitch, dpitch;
@@ -355,90 +475,88 @@ struct ScaleOp {
     s = sbase + r * spitch;
     d = dbase + r * dpitch;
   }
-  __device__ __forceinline__ int lead() const { return lead4<D>(d); }
+  __device__ __forceinline__ int head() const { return lead<D>(d, kGroup * kSize<D>); }
   __device__ __forceinline__ void one(int j) {
     store1<D>(d + (int64_t)j * kSize<D>, (load1<S>(s + (int64_t)j * kSize<S>) * inv) * coef);
   }
   template <int U, int W, bool FULL>
-  __device__ __forceinline__ void groups(int head, int q, int ng) {
-    Raw4<S> x[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) x[k] = load4<S>(s + group_at<FULL>(head, q + k * W, ng) * kSize<S>);
+  __device__ __forceinline__ void groups(int first, int q, int ng) {
+    Raw<S, kGroup> x[U];
 #pragma unroll
     for (int k = 0; k < U; ++k)
-      if (FULL || q + k * W < ng)
-        store4<D>(d + (int64_t)(head + 4 * (q + k * W)) * kSize<D>, (decode4<S>(x[k]) * inv) * coef);
+      x[k] = load<S, kGroup, NT>(s + group_at<kGroup, FULL>(first, q + k * W, ng) * kSize<S>);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (!FULL && q + k * W >= ng) continue;
+      Raw<D, kGroup> y;
+      const f32x4 lo = (decode4(x[k], 0) * inv) * coef;
+      if constexpr (D == ZERO_F32) {
+        y.r = lo;
+      } else if constexpr (kGroup == 4) {
+        y.r = encode4<D>(lo);
+      } else {
+        const u32x2 a = encode4<D>(lo), b = encode4<D>((decode4(x[k], 1) * inv) * coef);
+        y.r = u32x4{a.x, a.y, b.x, b.y};
+      }
+      typedef ZS_GLOBAL typename Raw<D, kGroup>::V* ptr;
+      const ptr to = (ptr)(d + (int64_t)(first + kGroup * (q + k * W)) * kSize<D>);
+      if constexpr (NT) __builtin_nontemporal_store(y.r, to);
+      else *to = y.r;
+    }
   }
 };
 
-template <int S, int D, int W>
+template <int S, int D, int W, bool NT>
 __device__ __forceinline__ void scale_item(const GradsChunk& k, float inv, float coef, int t) {
   const src_t s = (src_t)k.src;
   const dst_t d = (dst_t)k.dst;
-  ScaleOp<S, D> op{s, d, k.src_pitch, k.dst_pitch, inv, coef, s, d};
-  walk_item<W, 4>(op, k, t);
+  ScaleOp<S, D, NT> op{s, d, k.src_pitch, k.dst_pitch, inv, coef, s, d};
+  walk_item<W, W == 64 || (S != ZERO_F32 && D != ZERO_F32) ? 2 : 1>(op, k, t);
 }
-template <int S, int W>
+template <int S, int W, bool NT>
 __device__ __forceinline__ void scale_to(const GradsChunk& k, float inv, float coef, int t) {
-  if (k.dst_dtype == ZERO_F32) scale_item<S, ZERO_F32, W>(k, inv, coef, t);
-  else if (k.dst_dtype == ZERO_BF16) scale_item<S, ZERO_BF16, W>(k, inv, coef, t);
-  else scale_item<S, ZERO_F16, W>(k, inv, coef, t);
+  if (k.dst_dtype == ZERO_F32) scale_item<S, ZERO_F32, W, NT>(k, inv, coef, t);
+  else if (k.dst_dtype == ZERO_BF16) scale_item<S, ZERO_BF16, W, NT>(k, inv, coef, t);
+  else scale_item<S, ZERO_F16, W, NT>(k, inv, coef, t);
 }
-template <int W>
+template <int W, bool NT>
 __device__ __forceinline__ void scale_any(const GradsChunk& k, float inv, float coef, int t) {
-  if (inv == 1.0f && coef == 1.0f && k.src == k.dst) return;  // in place and nothing to change
-  if (k.src_dtype == ZERO_F32) scale_to<ZERO_F32, W>(k, inv, coef, t);
-  else if (k.src_dtype == ZERO_BF16) scale_to<ZERO_BF16, W>(k, inv, coef, t);
-  else scale_to<ZERO_F16, W>(k, inv, coef, t);
+  if (k.src_dtype == ZERO_F32) scale_to<ZERO_F32, W, NT>(k, inv, coef, t);
+  else if (k.src_dtype == ZERO_BF16) scale_to<ZERO_BF16, W, NT>(k, inv, coef, t);
+  else scale_to<ZERO_F16, W, NT>(k, inv, coef, t);
 }
 
-struct ClipArgs {
-  int32_t kind, scope;
-  float inv, max_norm;
-  int32_t other_flag;
-  double other_acc;
-};
-
-__device__ __forceinline__ float coefficient(double norm, bool bad, float max_norm) {
-  if (bad || !(max_norm > 0.0f)) return 1.0f;
-  const double c = (double)max_norm / (norm + 1e-6);
-  return c < 1.0 ? (float)c : 1.0f;
-}
-
-// CLIP: the coefficient from the device-resident results, computed alike by every block;
-// else a plain scaling by c.inv.
-template <bool CLIP>
-__global__ void __launch_bounds__(kGradsBlock) grads_scale_kernel(GradsArgs a, ClipArgs c) {
-  float coef = 1.0f;
-  bool bad = false;
-  if constexpr (CLIP) {
-    double acc = a.sc->acc;
-    if (c.kind == ZERO_NORM_L2) acc += c.other_acc;
-    else acc = c.other_acc > acc || __builtin_isnan(c.other_acc) ? c.other_acc : acc;
-    const double norm = c.kind == ZERO_NORM_L2 ? sqrt(acc) : acc;
-    bad = (a.sc->flag | c.other_flag) != 0 || !__builtin_isfinite(acc);
-    if (c.scope == ZERO_CLIP_GLOBAL) coef = coefficient(norm, bad, c.max_norm);
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-      a.sc->norm = (float)norm;
-      a.sc->coef = coef;
-      a.sc->clip_norm = norm;
-      a.sc->clip_flag = bad;
-    }
-  }
+// One of `parts` parts of a block item per block, or four wave items; by inv and, for a clip,
+// the coefficients found for it.
+__global__ void __launch_bounds__(kGradsBlock) grads_scale_kernel(GradsArgs a, float inv, int scope, int parts) {
   const int b = (int)blockIdx.x;
-  int i = b;
-  const bool by_wave = b >= a.n_block_items;
-  if (by_wave)
-    i = a.n_block_items + (b - a.n_block_items) * kGradsWaves +
-        __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int whole = a.n_block_items * parts;
+  const bool by_wave = b >= whole;
+  const int i = by_wave ? a.n_block_items + (b - whole) * kGradsWaves +
+                              __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6)
+                        : b / parts;
   if (i >= a.n_chunks) return;
-  const GradsChunk k = a.chunks[i];
-  if (CLIP && c.scope == ZERO_CLIP_EACH) {
-    const double acc = a.tensor_acc[k.tensor];
-    coef = coefficient(c.kind == ZERO_NORM_L2 ? sqrt(acc) : acc, bad, c.max_norm);
+  GradsChunk k = a.chunks[i];
+  const float coef = scope == ZERO_CLIP_GLOBAL ? a.sc->coef : scope == ZERO_CLIP_EACH ? a.coefs[k.tensor] : 1.0f;
+  if (inv == 1.0f && coef == 1.0f && k.src == k.dst) return;  // in place and nothing to change
+  if (by_wave) {
+    scale_any<64, false>(k, inv, coef, (int)threadIdx.x & 63);
+    return;
   }
-  if (by_wave) scale_any<64>(k, c.inv, coef, (int)threadIdx.x & 63);
-  else scale_any<kGradsBlock>(k, c.inv, coef, (int)threadIdx.x);
+  // the part: of a run, or whole rows
+  const int n = k.rows == 1 ? kGradsChunk / parts : (k.rows + parts - 1) / parts;
+  const int lo = b % parts * n, have = (k.rows == 1 ? k.cols : k.rows) - lo;
+  if (have <= 0) return;
+  if (k.rows == 1) {
+    k.cols = have < n ? have : n;
+    k.src += (uint64_t)(lo * (k.src_dtype == ZERO_F32 ? 4 : 2));
+    k.dst += (uint64_t)(lo * (k.dst_dtype == ZERO_F32 ? 4 : 2));
+  } else {
+    k.rows = have < n ? have : n;
+    k.src += (uint64_t)(lo * k.src_pitch);
+    k.dst += (uint64_t)(lo * k.dst_pitch);
+  }
+  scale_any<kGradsBlock, true>(k, inv, coef, (int)threadIdx.x);
 }
 
 // New addresses for up to kGradsBind tensors, one block per tensor.
@@ -471,38 +589,69 @@ hipError_t launch_grads_arm(const GradsArgs& a, hipStream_t st) {
 }
 
 template <int KIND>
-static hipError_t launch_norm(const GradsArgs& a, float inv, bool per_tensor, hipStream_t st) {
-  if (a.n_blocks == 0) hipLaunchKernelGGL(grads_empty_kernel, dim3(1), dim3(1), 0, st, a.sc);
-  else hipLaunchKernelGGL(grads_norm_kernel<KIND>, dim3(a.n_blocks), dim3(kGradsBlock), 0, st, a, inv);
+static hipError_t launch_norm(const GradsArgs& a, float inv, bool per_tensor, const ClipArgs& c, hipStream_t st) {
+  if (a.n_blocks == 0) {
+    hipLaunchKernelGGL(grads_empty_kernel, dim3(1), dim3(1), 0, st, a.sc, c);
+  } else {
+    const int per = a.n_block_items >= ZS_GRADS_PER_MIN ? ZS_GRADS_PER : 1;
+    const int runs = (a.n_block_items + per - 1) / per;
+    const unsigned g = (unsigned)(runs + (a.n_blocks - a.n_block_items));
+    uint64_t* parts = per_tensor ? a.item_part : nullptr;
+    if (a.bytes_in > ZS_GRADS_NT_BYTES)
+      hipLaunchKernelGGL((grads_norm_kernel<KIND, true>), dim3(g), dim3(kGradsBlock), 0, st, a, inv, per, runs, parts, c);
+    else
+      hipLaunchKernelGGL((grads_norm_kernel<KIND, false>), dim3(g), dim3(kGradsBlock), 0, st, a, inv, per, runs, parts, c);
+  }
   if (per_tensor) {
-    if (a.max_count <= 256)
+    if (a.max_count <= 64)
       hipLaunchKernelGGL((grads_tensor_norms_kernel<KIND, 64>), dim3((a.n_tensors - 1) / kGradsWaves + 1), dim3(kGradsBlock),
-                         0, st, a);
+                         0, st, a, c);
     else
       hipLaunchKernelGGL((grads_tensor_norms_kernel<KIND, kGradsBlock>), dim3(a.n_tensors), dim3(kGradsBlock), 0, st,
-                         a);
+                         a, c);
   }
   return hipGetLastError();
 }
 
-hipError_t launch_grads_norm(const GradsArgs& a, int kind, float inv, bool per_tensor, hipStream_t st) {
-  return kind == ZERO_NORM_MAX ? launch_norm<ZERO_NORM_MAX>(a, inv, per_tensor, st)
-                               : launch_norm<ZERO_NORM_L2>(a, inv, per_tensor, st);
+static hipError_t launch_norm_of(const GradsArgs& a, int norm, float inv, bool per_tensor, const ClipArgs& c,
+                                 hipStream_t st) {
+  return norm == ZERO_NORM_MAX ? launch_norm<ZERO_NORM_MAX>(a, inv, per_tensor, c, st)
+                               : launch_norm<ZERO_NORM_L2>(a, inv, per_tensor, c, st);
 }
 
-hipError_t launch_grads_clip(const GradsArgs& a, int kind, int scope, float inv, int other_flag, double other_acc,
-                             float max_norm, hipStream_t st) {
-  const ClipArgs c{kind, scope, inv, max_norm, other_flag, other_acc};
-  const unsigned g = a.n_blocks > 0 ? (unsigned)a.n_blocks : 1u;
-  hipLaunchKernelGGL(grads_scale_kernel<true>, dim3(g), dim3(kGradsBlock), 0, st, a, c);
+// scope 0: by inv alone.
+static hipError_t launch_scaling(const GradsArgs& a, float inv, int scope, hipStream_t st) {
+  if (a.n_blocks == 0) return hipSuccess;
+  // A block for 8 KiB of the wider side: short-lived blocks of one or two groups per lane keep
+  // reads and writes in step (bf16 to bf16, 1.56e9 elements: 1156 us with whole items, 1012
+  // with halves, 1030 with quarters; fp32 to bf16, 4.1e8: 445, 415 and 361; eighths 1350 and 450).
+  const int parts = a.all16 ? 2 : 4;
+  const unsigned g = (unsigned)(a.n_blocks + (int64_t)a.n_block_items * (parts - 1));
+  hipLaunchKernelGGL(grads_scale_kernel, dim3(g), dim3(kGradsBlock), 0, st, a, inv, scope, parts);
   return hipGetLastError();
+}
+
+hipError_t launch_grads_norm(const GradsArgs& a, int norm, float inv, bool per_tensor, hipStream_t st) {
+  return launch_norm_of(a, norm, inv, per_tensor, ClipArgs{}, st);
+}
+
+hipError_t launch_grads_clip(const GradsArgs& a, int norm, int scope, float inv, int other_flag, double other_acc,
+                             float max_norm, hipStream_t st) {
+  const ClipArgs c{1, norm, scope, max_norm, other_flag, other_acc};
+  const unsigned g = scope == ZERO_CLIP_EACH ? (unsigned)((a.n_tensors - 1) / kGradsBlock + 1) : 1u;
+  hipLaunchKernelGGL(grads_coefs_kernel, dim3(g), dim3(kGradsBlock), 0, st, a, c);
+  return launch_scaling(a, inv, scope, st);
+}
+
+hipError_t launch_grads_clip_norm(const GradsArgs& a, int norm, float inv, bool per_tensor, int scope, float max_norm,
+                                  hipStream_t st) {
+  const ClipArgs c{1, norm, scope, max_norm, 0, 0.0};
+  hipError_t e = launch_norm_of(a, norm, inv, per_tensor, c, st);
+  return e != hipSuccess ? e : launch_scaling(a, inv, scope, st);
 }
 
 hipError_t launch_grads_scale(const GradsArgs& a, float factor, hipStream_t st) {
-  if (a.n_blocks == 0) return hipSuccess;
-  const ClipArgs c{0, 0, factor, 0.0f, 0, 0.0};
-  hipLaunchKernelGGL(grads_scale_kernel<false>, dim3(a.n_blocks), dim3(kGradsBlock), 0, st, a, c);
-  return hipGetLastError();
+  return launch_scaling(a, factor, 0, st);
 }
 
 hipError_t launch_grads_bind(const GradsBindArgs& a, int n, hipStream_t st) {

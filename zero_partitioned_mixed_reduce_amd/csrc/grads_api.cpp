@@ -62,13 +62,14 @@ zero_status_t init(const zero_grads_tensor_t* tensors, int64_t n, void* workspac
   a.sc = reinterpret_cast<zs::GradsScalars*>(ws);
   a.tensor_acc = reinterpret_cast<double*>(ws + p.layout.tensor_acc);
   a.norms = reinterpret_cast<float*>(ws + p.layout.norms);
+  a.coefs = reinterpret_cast<float*>(ws + p.layout.coefs);
   a.part = reinterpret_cast<uint64_t*>(ws + p.layout.part);
-  a.wave_part = reinterpret_cast<uint64_t*>(ws + p.layout.wave_part);
+  a.item_part = reinterpret_cast<uint64_t*>(ws + p.layout.item_part);
   a.gcount = reinterpret_cast<uint32_t*>(ws + p.layout.gcount);
   a.gpart = reinterpret_cast<uint64_t*>(ws + p.layout.gpart);
   a.max_count = p.max_count;
   a.bytes_in = p.bytes_in;
-  a.bytes_out = p.bytes_out;
+  a.all16 = p.all16;
   const zs::GradsScalars sc = {};
   zero_status_t rs = ZERO_OK;
   if ((e = hipMemcpyAsync(a.sc, &sc, sizeof(sc), hipMemcpyHostToDevice, st)) != hipSuccess)
@@ -157,24 +158,6 @@ zero_status_t check_clip(int32_t scope, float max_norm) {
   return ZERO_OK;
 }
 
-zero_status_t run_norm(zero_grads_t h, int32_t norm, float inv, bool per_tensor, hipStream_t st) {
-  hipError_t e = zs::launch_grads_norm(h->args, norm, inv, per_tensor, st);
-  if (e != hipSuccess) return hip_fail("norm kernel", e);
-  h->has_norm = true;
-  h->per_tensor = per_tensor;
-  h->norm = norm;
-  h->inv = inv;
-  return ZERO_OK;
-}
-zero_status_t run_clip(zero_grads_t h, int32_t scope, int32_t other_flag, double other_acc, float max_norm,
-                       hipStream_t st) {
-  hipError_t e = zs::launch_grads_clip(h->args, h->norm, scope, h->inv, other_flag != 0, other_acc, max_norm, st);
-  if (e != hipSuccess) return hip_fail("clip kernel", e);
-  h->has_norm = false;
-  h->clipped = true;
-  return ZERO_OK;
-}
-
 }  // namespace
 
 extern "C" {
@@ -222,7 +205,13 @@ zero_status_t zero_grads_norm(zero_grads_t h, int32_t norm, float inv_loss_scale
   zero_status_t s = check_norm(h, norm, inv_loss_scale);
   if (s != ZERO_OK) return s;
   DeviceGuard dg(h->device);
-  return run_norm(h, norm, inv_loss_scale, per_tensor != 0, static_cast<hipStream_t>(stream));
+  hipError_t e = zs::launch_grads_norm(h->args, norm, inv_loss_scale, per_tensor != 0, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail("norm kernel", e);
+  h->has_norm = true;
+  h->per_tensor = per_tensor != 0;
+  h->norm = norm;
+  h->inv = inv_loss_scale;
+  return ZERO_OK;
 }
 
 zero_status_t zero_grads_device(zero_grads_t h, double** acc, int32_t** found_inf, float** norm, double** tensor_acc,
@@ -247,7 +236,12 @@ zero_status_t zero_grads_clip(zero_grads_t h, int32_t scope, int32_t other_ranks
   if (scope == ZERO_CLIP_EACH && !h->per_tensor)
     return fail(ZERO_ESTATE, "ZERO_CLIP_EACH needs a zero_grads_norm with per_tensor");
   DeviceGuard dg(h->device);
-  return run_clip(h, scope, other_ranks_found_inf, other_ranks_acc, max_norm, static_cast<hipStream_t>(stream));
+  hipError_t e = zs::launch_grads_clip(h->args, h->norm, scope, h->inv, other_ranks_found_inf != 0, other_ranks_acc,
+                                       max_norm, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail("clip kernel", e);
+  h->has_norm = false;
+  h->clipped = true;
+  return ZERO_OK;
 }
 
 zero_status_t zero_grads_clip_norm(zero_grads_t h, int32_t norm, float inv_loss_scale, int32_t per_tensor,
@@ -257,10 +251,12 @@ zero_status_t zero_grads_clip_norm(zero_grads_t h, int32_t norm, float inv_loss_
   if (s == ZERO_OK) s = check_writable(h);
   if (s != ZERO_OK) return s;
   DeviceGuard dg(h->device);
-  hipStream_t st = static_cast<hipStream_t>(stream);
-  s = run_norm(h, norm, inv_loss_scale, per_tensor != 0 || scope == ZERO_CLIP_EACH, st);
-  if (s != ZERO_OK) return s;
-  return run_clip(h, scope, 0, 0.0, max_norm, st);
+  hipError_t e = zs::launch_grads_clip_norm(h->args, norm, inv_loss_scale, per_tensor != 0 || scope == ZERO_CLIP_EACH,
+                                            scope, max_norm, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail("norm and clip kernels", e);
+  h->has_norm = false;
+  h->clipped = true;
+  return ZERO_OK;
 }
 
 zero_status_t zero_grads_scale(zero_grads_t h, float factor, void* stream) {

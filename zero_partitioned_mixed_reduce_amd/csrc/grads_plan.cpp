@@ -126,14 +126,15 @@ zero_status_t build_grads_plan(const zero_grads_tensor_t* tensors, int64_t n, Gr
     return ZERO_EINVAL;
   }
   if (n < 1 || n > kGradsMaxBlocks) {
-    *err = "need 1 <= n <= 2^24 - 1 tensors";
+    *err = "need 1 <= n <= 2^22 - 1 tensors";
     return ZERO_EINVAL;
   }
   GradsPlan p;
   p.tensors.assign(tensors, tensors + n);
   p.in_place.resize((size_t)n);
   memset(&p.info, 0, sizeof(p.info));
-  p.bytes_in = p.bytes_out = 0;
+  p.bytes_in = 0;
+  p.all16 = true;
   for (int64_t i = 0; i < n; ++i) {
     zero_grads_tensor_t& t = p.tensors[i];
     if (!known(t.src_dtype)) return bad(err, i, "src_dtype must be ZERO_F16, ZERO_BF16 or ZERO_F32");
@@ -167,7 +168,7 @@ zero_status_t build_grads_plan(const zero_grads_tensor_t* tensors, int64_t n, Gr
       t.src_pitch = t.dst_pitch = len;
     }
     p.bytes_in += len * size_of(t.src_dtype);
-    p.bytes_out += len * size_of(t.dst_dtype);
+    p.all16 = p.all16 && (len == 0 || (t.src_dtype != ZERO_F32 && t.dst_dtype != ZERO_F32));
   }
   zero_status_t s = check_grads_addresses(p.tensors, p.in_place, &p.overlap, err);
   if (s != ZERO_OK) return s;
@@ -186,7 +187,7 @@ zero_status_t build_grads_plan(const zero_grads_tensor_t* tensors, int64_t n, Gr
   for (const auto& t : p.tensors) {
     const int64_t c = count_of(t);
     if (c > kGradsMaxBlocks || n_block > kGradsMaxBlocks) {
-      *err = "the list needs more than 2^24 - 1 blocks of work";
+      *err = "the list needs more than 2^22 - 1 blocks of work";
       return ZERO_EINVAL;
     }
     (is_small(t) ? n_wave : n_block) += c;
@@ -194,7 +195,7 @@ zero_status_t build_grads_plan(const zero_grads_tensor_t* tensors, int64_t n, Gr
   }
   const int64_t n_blocks = n_block + (n_wave + kGradsWaves - 1) / kGradsWaves;
   if (n_blocks > kGradsMaxBlocks) {
-    *err = "the list needs more than 2^24 - 1 blocks of work";
+    *err = "the list needs more than 2^22 - 1 blocks of work";
     return ZERO_EINVAL;
   }
   p.n_block_items = n_block;
@@ -206,9 +207,10 @@ zero_status_t build_grads_plan(const zero_grads_tensor_t* tensors, int64_t n, Gr
   l.ranges = up(l.chunks + p.info.num_chunks * (int64_t)sizeof(GradsChunk));
   l.tensor_acc = up(l.ranges + n * (int64_t)sizeof(GradsRange));
   l.norms = up(l.tensor_acc + 8 * n);
-  l.part = up(l.norms + 4 * n);
-  l.wave_part = up(l.part + 8 * n_blocks);
-  l.gcount = up(l.wave_part + 8 * n_wave);
+  l.coefs = up(l.norms + 4 * n);
+  l.part = up(l.coefs + 4 * n);
+  l.item_part = up(l.part + 8 * n_blocks);
+  l.gcount = up(l.item_part + 8 * (n_block * kGradsWaves + n_wave));
   l.gpart = up(l.gcount + 64 * grads_groups(n_blocks));
   l.end = up(l.gpart + 8 * grads_groups(n_blocks));
   p.info.workspace_bytes = l.end;

@@ -91,11 +91,20 @@ class ZeroGrads:
         if not self._tensors:
             raise ValueError("an empty list")
         self._in_place = out is None
-        self._out = dsts = self._check(self._tensors, out)
-        self.device = self._tensors[0].device
+        dsts = self._check(self._tensors, out)
+        self._out = out
+        self.device = self._tensors[0].device   # with its index
         desc = (abi.zero_grads_tensor_t * len(self._tensors))(
             *[describe(i, s, d) for i, (s, d) in enumerate(zip(self._tensors, dsts))])
-        self._layout = [self._signature(s, d) for s, d in zip(self._tensors, dsts)]
+        self._layout = [self._signature(t) for t in self._tensors]
+        self._out_layout = None if out is None else [self._signature(t) for t in dsts]
+        self._flat = isinstance(out, torch.Tensor)
+        if self._flat:
+            self._out_dtype, self._total, size, at = out.dtype, out.numel(), out.element_size(), 0
+            self._offsets = []
+            for t in self._tensors:
+                self._offsets.append(at)
+                at += t.numel() * size
         self.info = abi.zero_grads_plan(desc)
         self.h = None
         with torch.cuda.device(self.device):
@@ -111,8 +120,20 @@ class ZeroGrads:
         self.tensor_acc, self.norms = views[3:]
 
     @staticmethod
-    def _signature(s, d):
-        return (s.dtype, s.shape, s.stride(), None if d is None else (d.dtype, d.shape, d.stride()))
+    def _signature(t):
+        """What a tensor bound later has to have in common: dtype, size, and for one that is not contiguous its shape
+        and strides."""
+        return (t.dtype, t.numel(), None if t.is_contiguous() else (t.shape, t.stride()))
+
+    def _addresses(self, tensors, layout, what):
+        """The tensors' addresses, once each is what the plan has in its place."""
+        dev, ptrs = self.device.index, []
+        for t, (dtype, numel, strides) in zip(tensors, layout):
+            if (t.dtype is not dtype or t.numel() != numel or t.get_device() != dev
+                    or (not t.is_contiguous() if strides is None else (t.shape, t.stride()) != strides)):
+                raise ValueError(f"{what} {len(ptrs)}: dtype, sizes, strides or device differ from the plan's")
+            ptrs.append(t.data_ptr())
+        return ptrs
 
     def _check(self, tensors, out):
         """Checks a list and returns its destinations, one per tensor (None: in place)."""
@@ -141,7 +162,7 @@ class ZeroGrads:
         return dsts
 
     def _stream(self):
-        return ctypes.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
 
     # calls of the C ABI, under its names
     def zero_grads_bind(self, tensors, out=None):
@@ -150,16 +171,24 @@ class ZeroGrads:
         if len(tensors) != len(self._layout):
             raise ValueError(f"the plan has {len(self._layout)} tensors, got {len(tensors)}")
         if (out is None) != self._in_place:
-            raise ValueError("the plan is " + ("in place: bind without out" if self._in_place else "not in place: bind with out"))
-        dsts = self._check(tensors, out)
-        if tensors[0].device != self.device:
-            raise ValueError(f"the plan is on {self.device}, the tensors on {tensors[0].device}")
-        for i, (s, d) in enumerate(zip(tensors, dsts)):
-            if self._signature(s, d) != self._layout[i]:
-                raise ValueError(f"tensor {i}: dtype, shape or strides differ from the plan's")
-        abi.zero_grads_bind(self.h, [t.data_ptr() for t in tensors],
-                            None if out is None else [t.data_ptr() for t in dsts], self._stream())
-        self._tensors, self._out = tensors, dsts
+            raise ValueError("the plan is in place: bind without out" if self._in_place
+                             else "the plan is not in place: bind with out")
+        if isinstance(out, torch.Tensor) != self._flat:
+            raise ValueError("out is one flat tensor in the plan or a list in the plan, and not the other here")
+        src, dst = self._addresses(tensors, self._layout, "tensor"), None
+        if self._flat:
+            if (out.dtype is not self._out_dtype or out.numel() != self._total or not out.is_contiguous()
+                    or out.get_device() != self.device.index):
+                raise ValueError("out: dtype, size, strides or device differ from the plan's")
+            base = out.data_ptr()
+            dst = [base + o for o in self._offsets]
+        elif out is not None:
+            out = list(out)
+            if len(out) != len(tensors):
+                raise ValueError(f"{len(tensors)} tensors, {len(out)} out tensors")
+            dst = self._addresses(out, self._out_layout, "out")
+        abi.zero_grads_bind(self.h, src, dst, self._stream())
+        self._tensors, self._out = tensors, out
 
     def zero_grads_norm(self, norm=abi.ZERO_NORM_L2, inv_loss_scale=1.0, per_tensor=False):
         abi.zero_grads_norm(self.h, norm, inv_loss_scale, per_tensor, self._stream())
