@@ -245,7 +245,8 @@ int main() {
     if (zs::build_grads_plan(t.data(), n, &p, &err) != ZERO_OK) { printf("refused: %s\n", err.c_str()); return 1; }
     zs::fill_grads_chunks(&p);
     if (p.info.elems != elems || (int64_t)p.chunks.size() != p.info.num_chunks) { printf("bad sizes\n"); return 1; }
-    int64_t covered_items = 0;
+    int64_t covered_items = 0, join = 0;
+    auto joins = [](int64_t c) { return c <= 1 ? 0 : (c + 63) / 64 + (c > 64); };
     for (int i = 0; i < n; ++i) {
       zero_grads_tensor_t x = t[i];
       if (!x.dst) { x.dst = x.src; x.dst_pitch = x.src_pitch; x.dst_dtype = x.src_dtype; }
@@ -255,15 +256,18 @@ int main() {
       for (int c = p.ranges[i].first; c < p.ranges[i].first + p.ranges[i].count; ++c) {
         const zs::GradsChunk& k = p.chunks[c];
         if ((c >= p.n_block_items) != wave || k.tensor != i || k.src_dtype != x.src_dtype || k.dst_dtype != x.dst_dtype) { printf("bad item\n"); return 1; }
-        if (k.src_off != (int64_t)(k.src - (uint64_t)(uintptr_t)x.src) || k.dst_off != (int64_t)(k.dst - (uint64_t)(uintptr_t)x.dst)) { printf("bad offset\n"); return 1; }
+        if (p.offsets[c].src != (int64_t)(k.src - (uint64_t)(uintptr_t)x.src) || p.offsets[c].dst != (int64_t)(k.dst - (uint64_t)(uintptr_t)x.dst)) { printf("bad offset\n"); return 1; }
+        if (k.first != p.ranges[i].first || k.count != p.ranges[i].count || (k.count > 1 && (k.join != join || k.join + joins(k.count) > p.n_joins))) { printf("bad joins\n"); return 1; }
         if ((int64_t)k.rows * k.cols > zs::kGradsChunk || k.rows < 1 || k.cols < 1) { printf("bad size\n"); return 1; }
         for (int r = 0; r < k.rows; ++r)
           for (int e = 0; e < k.cols; ++e)
             got.push_back({k.src + r * k.src_pitch + (uint64_t)e * es(k.src_dtype), k.dst + r * k.dst_pitch + (uint64_t)e * es(k.dst_dtype)});
         ++covered_items;
       }
+      join += joins(p.ranges[i].count);
       if (got != want) { printf("tensor %d not covered in order\n", i); return 1; }
     }
+    if (join != p.n_joins) { printf("bad counters\n"); return 1; }
     const int64_t n_wave = p.info.num_chunks - p.n_block_items;
     if (covered_items != p.info.num_chunks || p.n_blocks != p.n_block_items + (n_wave + 3) / 4) { printf("bad blocks\n"); return 1; }
     ++tables;

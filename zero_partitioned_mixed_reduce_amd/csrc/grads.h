@@ -23,8 +23,10 @@ static_assert(kGradsChunk % 8 == 0, "chunk starts keep a tensor's alignment");
 constexpr int kGradsSmall = ZS_GRADS_SMALL;
 constexpr int kGradsBlock = 256;
 constexpr int kGradsWaves = kGradsBlock / 64;
-// Blocks whose partial results one group combines (see grads_finish).
-constexpr int kGradsGroup = 256;
+// Consecutive block items that a block of the norm kernel takes at most.
+constexpr int kGradsRun = 4;
+// Items of one tensor whose results a wave joins at once.
+constexpr int kGradsJoin = 64;
 // Limit of the blocks of work (each up to four blocks of a launch, whose limit is 2^32 - 1
 // threads) and of the tensors.
 constexpr int64_t kGradsMaxBlocks = (1 << 22) - 1;
@@ -33,15 +35,22 @@ constexpr int64_t kGradsMaxBlocks = (1 << 22) - 1;
 // wave items, each in list order.
 struct alignas(64) GradsChunk {
   uint64_t src, dst;              // addresses of the first element
-  int64_t src_off, dst_off;       // their byte offsets in the tensor
   int64_t src_pitch, dst_pitch;   // bytes from row to row
   int32_t rows, cols;
   int32_t tensor;
   int16_t src_dtype, dst_dtype;
+  int32_t first, count;           // the tensor's items: [first, first + count) of the table
+  int32_t join;                   // index of the tensor's first counter and group result
+  int32_t pad;
 };
 static_assert(sizeof(GradsChunk) == 64, "work item layout");
 
-// A tensor's work items: [first, first + count) of the table.
+// An item's first element in its tensor, in bytes.
+struct GradsOffset {
+  int64_t src, dst;
+};
+
+// A tensor's items: [first, first + count) of the table.
 struct GradsRange {
   int32_t first, count;
 };
@@ -50,7 +59,7 @@ struct GradsRange {
 struct alignas(256) GradsScalars {
   double acc;        // sum of squares, or the largest magnitude
   int32_t flag;      // acc is not finite
-  uint32_t counter;  // groups that have completed (re-armed by the last)
+  uint32_t counter;  // groups of blocks that have completed (re-armed by the last)
   float norm;        // in fp32; the one clipped by after a clip
   float coef;        // global coefficient of the last clip
   double clip_norm;  // global norm of the last clip
@@ -63,7 +72,7 @@ static_assert(sizeof(GradsScalars) == 256, "scalar block");
 enum GradsInto : uint8_t { kInto = 0, kInPlace = 1, kInPlaceGiven = 2 };
 
 struct GradsLayout {
-  int64_t chunks, ranges, tensor_acc, norms, coefs, part, item_part, gcount, gpart, end;
+  int64_t chunks, offsets, ranges, tensor_acc, norms, coefs, part, item_part, gcount, gpart, join_count, join_part, end;
 };
 
 struct GradsPlan {
@@ -72,10 +81,14 @@ struct GradsPlan {
   std::vector<uint8_t> in_place;             // kInto, kInPlace or kInPlaceGiven
   int64_t overlap;                           // a tensor with no destination that shares elements with another, or -1
   std::vector<GradsChunk> chunks;
+  std::vector<GradsOffset> offsets;
   std::vector<GradsRange> ranges;
   int64_t n_block_items;  // the rest are wave items
-  int64_t n_blocks;
-  int64_t max_count;      // work items of the largest tensor
+  int64_t n_blocks;       // of one block item or kGradsWaves wave items each
+  int64_t run;            // block items per block of the norm kernel
+  int64_t norm_grid;      // blocks of the norm kernel
+  int64_t group;          // blocks of the norm kernel whose results one group joins
+  int64_t n_joins;        // counters of the tensors of several items
   int64_t bytes_in;       // of the sources
   bool all16;             // every source and destination is 16-bit
   GradsLayout layout;
@@ -91,12 +104,11 @@ void fill_grads_chunks(GradsPlan* p);
 zero_status_t check_grads_addresses(const std::vector<zero_grads_tensor_t>& t, const std::vector<uint8_t>& in_place,
                                     int64_t* overlap, std::string* err);
 
-inline int64_t grads_groups(int64_t n_blocks) { return (n_blocks + kGradsGroup - 1) / kGradsGroup; }
-
 // Tensors whose new addresses one launch of the bind kernel carries (kernel arguments hold 4 KiB).
 constexpr int kGradsBind = 240;
 struct GradsBindArgs {
   GradsChunk* chunks;
+  const GradsOffset* offsets;
   const GradsRange* ranges;
   int32_t first;  // index of the first tensor
   uint64_t src[kGradsBind], dst[kGradsBind];
@@ -104,20 +116,20 @@ struct GradsBindArgs {
 
 struct GradsArgs {
   const GradsChunk* chunks;
-  int32_t n_block_items, n_chunks, n_blocks;
-  int32_t n_tensors;
-  const GradsRange* ranges;
   GradsScalars* sc;
   double* tensor_acc;
   float* norms;
-  float* coefs;         // of the last clip by each tensor's norm
-  uint64_t* part;       // one per block
-  uint64_t* item_part;  // one per wave of each block item, then one per wave item
-  uint32_t* gcount;     // one 64-byte line per group
-  uint64_t* gpart;      // one per group
-  int64_t max_count;
-  int64_t bytes_in;     // of the sources
-  int32_t all16;        // every source and destination is 16-bit
+  float* coefs;          // of the last clip by each tensor's norm
+  uint64_t* part;        // one per block of the norm kernel
+  uint64_t* item_part;   // one per item
+  uint32_t* gcount;      // one 64-byte line per group of blocks
+  uint64_t* gpart;       // one per group of blocks
+  uint32_t* join_count;  // one 64-byte line per kGradsJoin items of a tensor, and one more per tensor of several
+  uint64_t* join_part;   // beside them
+  int64_t bytes_in;      // of the sources
+  int32_t n_block_items, n_chunks, n_blocks, n_tensors;
+  int32_t run, group;
+  int32_t all16;         // every source and destination is 16-bit
 };
 
 }  // namespace zs

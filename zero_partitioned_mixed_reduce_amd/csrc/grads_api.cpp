@@ -54,11 +54,6 @@ zero_status_t init(const zero_grads_tensor_t* tensors, int64_t n, void* workspac
   char* ws = static_cast<char*>(workspace);
   zs::GradsArgs a;
   a.chunks = reinterpret_cast<zs::GradsChunk*>(ws + p.layout.chunks);
-  a.n_block_items = (int32_t)p.n_block_items;
-  a.n_chunks = (int32_t)p.info.num_chunks;
-  a.n_blocks = (int32_t)p.n_blocks;
-  a.n_tensors = (int32_t)n;
-  a.ranges = reinterpret_cast<zs::GradsRange*>(ws + p.layout.ranges);
   a.sc = reinterpret_cast<zs::GradsScalars*>(ws);
   a.tensor_acc = reinterpret_cast<double*>(ws + p.layout.tensor_acc);
   a.norms = reinterpret_cast<float*>(ws + p.layout.norms);
@@ -67,27 +62,42 @@ zero_status_t init(const zero_grads_tensor_t* tensors, int64_t n, void* workspac
   a.item_part = reinterpret_cast<uint64_t*>(ws + p.layout.item_part);
   a.gcount = reinterpret_cast<uint32_t*>(ws + p.layout.gcount);
   a.gpart = reinterpret_cast<uint64_t*>(ws + p.layout.gpart);
-  a.max_count = p.max_count;
+  a.join_count = reinterpret_cast<uint32_t*>(ws + p.layout.join_count);
+  a.join_part = reinterpret_cast<uint64_t*>(ws + p.layout.join_part);
   a.bytes_in = p.bytes_in;
+  a.n_block_items = (int32_t)p.n_block_items;
+  a.n_chunks = (int32_t)p.info.num_chunks;
+  a.n_blocks = (int32_t)p.n_blocks;
+  a.n_tensors = (int32_t)n;
+  a.run = (int32_t)p.run;
+  a.group = (int32_t)p.group;
   a.all16 = p.all16;
   const zs::GradsScalars sc = {};
   zero_status_t rs = ZERO_OK;
   if ((e = hipMemcpyAsync(a.sc, &sc, sizeof(sc), hipMemcpyHostToDevice, st)) != hipSuccess)
     rs = hip_fail("hipMemcpyAsync(scalars)", e);
   else if (!p.chunks.empty() &&
-           (e = hipMemcpyAsync(ws + p.layout.chunks, p.chunks.data(), p.chunks.size() * sizeof(zs::GradsChunk),
-                               hipMemcpyHostToDevice, st)) != hipSuccess)
+           ((e = hipMemcpyAsync(ws + p.layout.chunks, p.chunks.data(), p.chunks.size() * sizeof(zs::GradsChunk),
+                                hipMemcpyHostToDevice, st)) != hipSuccess ||
+            (e = hipMemcpyAsync(ws + p.layout.offsets, p.offsets.data(), p.offsets.size() * sizeof(zs::GradsOffset),
+                                hipMemcpyHostToDevice, st)) != hipSuccess))
     rs = hip_fail("hipMemcpyAsync(work table)", e);
   else if ((e = hipMemcpyAsync(ws + p.layout.ranges, p.ranges.data(), p.ranges.size() * sizeof(zs::GradsRange),
                                hipMemcpyHostToDevice, st)) != hipSuccess)
     rs = hip_fail("hipMemcpyAsync(tensor table)", e);
-  else if ((e = zs::launch_grads_arm(a, st)) != hipSuccess)
-    rs = hip_fail("group counters", e);
+  // the counters start at zero (and are re-armed by every pass); empty tensors' norms stay zero
+  else if ((e = zs::launch_fill_zero(reinterpret_cast<float*>(a.tensor_acc),
+                                     (p.layout.part - p.layout.tensor_acc) / (int64_t)sizeof(float), st)) != hipSuccess ||
+           (e = zs::launch_fill_zero(reinterpret_cast<float*>(a.gcount),
+                                     (p.layout.end - p.layout.gcount) / (int64_t)sizeof(float), st)) != hipSuccess)
+    rs = hip_fail("workspace fill", e);
   // copies already enqueued read the plan's tables
   e = hipStreamSynchronize(st);
   if (rs != ZERO_OK) return rs;
   if (e != hipSuccess) return hip_fail("hipStreamSynchronize(init)", e);
   p.chunks = std::vector<zs::GradsChunk>();
+  p.offsets = std::vector<zs::GradsOffset>();
+  p.ranges = std::vector<zs::GradsRange>();
   zero_grads* h = new (std::nothrow) zero_grads();
   if (!h) return fail(ZERO_ENOMEM, "out of host memory");
   h->plan = std::move(p);
@@ -121,7 +131,9 @@ zero_status_t bind(zero_grads_t h, void* const* src, void* const* dst, hipStream
   DeviceGuard dg(h->device);
   zs::GradsBindArgs a;
   a.chunks = const_cast<zs::GradsChunk*>(h->args.chunks);
-  a.ranges = h->args.ranges;
+  char* ws = reinterpret_cast<char*>(h->args.sc);
+  a.offsets = reinterpret_cast<zs::GradsOffset*>(ws + h->plan.layout.offsets);
+  a.ranges = reinterpret_cast<zs::GradsRange*>(ws + h->plan.layout.ranges);
   for (int64_t i = 0; i < n; i += zs::kGradsBind) {
     const int m = (int)(n - i < zs::kGradsBind ? n - i : zs::kGradsBind);
     a.first = (int32_t)i;

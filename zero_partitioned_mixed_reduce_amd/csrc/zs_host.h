@@ -56,7 +56,6 @@ hipError_t launch_adam_step(int dtype, int grad_source, bool cast, const Chunk* 
 
 // Kernel launchers of the gradient lists (grads.hip).
 namespace zs {
-hipError_t launch_grads_arm(const GradsArgs& a, hipStream_t st);
 hipError_t launch_grads_norm(const GradsArgs& a, int norm, float inv, bool per_tensor, hipStream_t st);
 hipError_t launch_grads_clip(const GradsArgs& a, int norm, int scope, float inv, int other_flag, double other_acc,
                              float max_norm, hipStream_t st);
