@@ -24,8 +24,9 @@
  * 65504 become infinite; a NaN is written to a 16-bit destination as the
  * format's positive canonical quiet NaN (see zero_cast_params).
  *
- * The sums are formed in an order fixed by the list's sizes: the same values
- * give the same bits, whatever else runs on the GPU.
+ * The sums are formed in an order fixed by the list's sizes and its tensors'
+ * alignment to 16 bytes: the same values there give the same bits, in every
+ * call and replay and whatever else runs on the GPU.
  *
  * Conventions are those of zero_shard.h (zero_status_t, zero_last_error(),
  * streams, caller-owned device memory), and:

@@ -138,6 +138,30 @@ def test_clip_types_and_offsets(src, dst):
         h.close()
 
 
+@pytest.mark.parametrize("src,dst", [(a, b) for a in DT for b in DT])
+def test_ends_of_parts(src, dst):
+    """Runs that end within a vector of an item's or a part's end, at every alignment of source and destination: every
+    element is written once, in place too, and none beside them; each norm counts each once."""
+    for extra in range(1, 10):
+        sizes = [2048 + extra, 4096 + extra, 8192 + extra, 6144 - extra, 16384 + extra]
+        for lead in range(8):
+            total = sum(sizes)
+            base = rand(extra, total + 16, src)
+            out = torch.full((total + 32,), 7.0, dtype=dst, device="cuda")
+            at = (3 * lead + extra) % 8
+            h = ZeroGrads(list(base[lead:lead + total].split(sizes)), out=out[at:at + total])
+            h.zero_grads_scale(float(np.float32(0.7)))
+            assert (bits(out[at:at + total]) == bits(emulate(base[lead:lead + total], 0.7, 1.0, dst))).all()
+            assert (out[:at] == 7).all() and (out[at + total:] == 7).all()
+            if src == dst:
+                ones = torch.full((total + 16,), 1.0, dtype=src, device="cuda")
+                h = ZeroGrads(list(ones[lead:lead + total].split(sizes)))
+                h.zero_grads_norm(per_tensor=True)
+                assert float(h.acc) == total and h.tensor_acc.tolist() == sizes
+                h.zero_grads_scale(3.0)
+                assert (ones[lead:lead + total] == 3).all() and (ones[:lead] == 1).all() and (ones[lead + total:] == 1).all()
+
+
 @pytest.mark.parametrize("dt", DT)
 def test_in_place_and_scale(dt):
     grads = [rand(3 + i, n, dt) for i, n in enumerate(SIZES)]
@@ -442,6 +466,28 @@ def test_exchange_on_the_host_and_on_the_device():
                 assert abs(float(h.norm) - ref["norm"]) <= H * ref["norm"]
                 for o, g in zip(h._out, part):
                     assert (bits(o) == bits(emulate(g, 1.0, q["coef"], torch.float32))).all()
+    # tensors cut across the ranks: their sums are exchanged as well, and each is clipped by its whole norm
+    for kind, limit in ((L2, 5e-3), (MAX, 1e-3)):
+        outs = [torch.empty_like(g) for g in grads]
+        one = ZeroGrads(grads, out=outs)
+        one.zero_grads_clip_norm(limit, kind, scope=EACH)
+        halves = [[g[: g.numel() // 2] for g in grads], [g[g.numel() // 2:] for g in grads]]
+        a, b = [ZeroGrads(part, out=[torch.empty_like(g) for g in part]) for part in halves]
+        for h in (a, b):
+            h.zero_grads_norm(kind, per_tensor=True)
+        for x, y in ((a.acc, b.acc), (a.tensor_acc, b.tensor_acc)):
+            joint = x + y if kind == L2 else torch.maximum(x, y)
+            x.copy_(joint)
+            y.copy_(joint)
+        for h in (a, b):
+            h.zero_grads_clip(limit, EACH)
+        for o, x, y in zip(outs, a._out, b._out):
+            # the coefficients may differ in fp64's last places and so by one step of fp32
+            assert ((torch.cat([x, y]).double() - o.double()).abs() <= 4 * H * o.double().abs()).all()
+        a.zero_grads_norm(kind, per_tensor=True)
+        a.zero_grads_clip(1e-6, EACH, other_ranks_found_inf=True)
+        assert all(torch.equal(o, g) for o, g in zip(a._out, halves[0])) and a.query()["found_inf"]
+    a = ZeroGrads(grads, out=[torch.empty_like(g) for g in grads])
     # another rank's flag, or a non-finite sum of its, stops the clip here
     for kw in (dict(other_ranks_found_inf=True), dict(other_ranks_acc=math.inf), dict(other_ranks_acc=math.nan)):
         for kind in (L2, MAX):
@@ -508,6 +554,40 @@ def test_other_stream():
         h.zero_grads_clip_norm(0.01)
         q = h.query()
     assert all((bits(a) == bits(b)).all() for a, b in zip(ref, h._out)) and not q["found_inf"]
+
+
+def test_two_handles_at_once():
+    """Two handles on two streams, each many times with nothing between: neither disturbs the other."""
+    lists = [ragged(k, 60, 40000) for k in (31, 32)]
+    hs = [ZeroGrads(g, out=torch.empty(sum(t.numel() for t in g), dtype=torch.bfloat16, device="cuda")) for g in lists]
+    refs = []
+    for h in hs:
+        h.zero_grads_clip_norm(0.01, per_tensor=True)
+        refs.append((h._out.clone(), h.acc.clone(), h.norms.clone()))
+        h._out.zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(50):
+        for h, s in zip(hs, streams):
+            with torch.cuda.stream(s):
+                h.zero_grads_clip_norm(0.01, per_tensor=True)
+    torch.cuda.synchronize()
+    for h, (o, acc, norms) in zip(hs, refs):
+        assert (bits(h._out) == bits(o)).all() and torch.equal(h.acc, acc) and torch.equal(h.norms, norms)
+
+
+def test_closed_handle_and_kept_tensors():
+    h = ZeroGrads([torch.ones(5000, device="cuda") for _ in range(3)])   # only the handle keeps them
+    for _ in range(4):
+        torch.zeros(5000, device="cuda")
+    h.zero_grads_norm()
+    assert float(h.acc) == 15000.0
+    h.close()
+    h.close()
+    for call in (h.zero_grads_norm, h.query, lambda: h.zero_grads_scale(1.0), lambda: h.zero_grads_clip_norm(1.0)):
+        with pytest.raises(ZeroError) as e:
+            call()
+        assert e.value.status == _abi.ZERO_EINVAL
 
 
 def test_beyond_32_bits():

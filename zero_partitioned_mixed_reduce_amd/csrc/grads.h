@@ -41,7 +41,9 @@ struct alignas(64) GradsChunk {
   int16_t src_dtype, dst_dtype;
   int32_t first, count;           // the tensor's items: [first, first + count) of the table
   int32_t join;                   // index of the tensor's first counter and group result
-  int32_t pad;
+  int16_t before, after;          // whether the item's run began before it, and how many of its elements
+                                  // follow (at most 7): an item begins and ends on vector boundaries
+                                  // inside a run, wherever the run itself begins
 };
 static_assert(sizeof(GradsChunk) == 64, "work item layout");
 

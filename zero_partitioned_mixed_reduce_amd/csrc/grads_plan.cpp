@@ -274,7 +274,8 @@ void fill_grads_chunks(GradsPlan* p) {
       k.dst_dtype = (int16_t)t.dst_dtype;
       k.first = (int32_t)first;
       k.join = (int32_t)join;
-      k.pad = 0;
+      k.before = c > 0;
+      k.after = (int16_t)std::min<int64_t>(7, t.cols - (c + cols));
     };
     if (len == 0) {
     } else if (len <= kGradsSmall) {
