@@ -18,7 +18,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libzero_shard.so")
-SOURCES = ["plan.cpp", "zero_shard_api.cpp", "kernels.hip", "grads_plan.cpp", "grads_api.cpp", "grads.hip"]
+SOURCES = ["plan.cpp", "zero_shard_api.cpp", "grads_plan.cpp", "grads_api.cpp", "device.hip"]  # kernels.hip, grads.hip
 HOST_SOURCES = ["offload.cpp"]
 HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

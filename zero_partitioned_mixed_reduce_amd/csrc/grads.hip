@@ -1,4 +1,4 @@
-// gfx950 kernels of the gradient-list operators.
+// gfx950 kernels of the gradient-list operators (compiled behind kernels.hip, see device.hip).
 //
 // All of them walk the list's work table: one or more items of at most kGradsChunk elements
 // per block, or a part of one, and four small tensors per block, one per wave.  They are
@@ -17,7 +17,6 @@
 #include <type_traits>
 
 #include "grads.h"
-#include "zs_device.h"
 #include "zs_internal.h"
 
 // Tuning knobs (each set to the value measured fastest on MI355X):
