@@ -266,6 +266,29 @@ def test_non_finite(value, kind, where):
     assert all((bits(a) == bits(b)).all() for a, b in zip(grads, plain))
 
 
+@pytest.mark.parametrize("src", DT)
+def test_nan_encoding(src):
+    """NaNs of both signs, with payloads, in vectors and at their ends: 16-bit destinations get the canonical one."""
+    g = rand(8, 3001, src)
+    raw = g.view(torch.int32 if src == torch.float32 else torch.int16)
+    for i, v in ((0, 0x7FC00001), (1, -0x3FFFFF), (500, 0x7F812345), (1501, -1), (3000, 0x7FFFFFFF)):
+        if src == torch.float16:
+            v = {0: 0x7E01, 1: -0x1FF, 500: 0x7C91, 1501: -1, 3000: 0x7FFF}[i]
+        elif src == torch.bfloat16:
+            v = {0: 0x7FC1, 1: -0x3F, 500: 0x7F81, 1501: -1, 3000: 0x7FFF}[i]
+        raw[i] = v
+    assert int(torch.isnan(g).sum()) == 5
+    for dst, canonical in ((torch.float16, 0x7E00), (torch.bfloat16, 0x7FC0)):
+        for lead in (0, 3):
+            out = torch.empty(3004, dtype=dst, device="cuda")[lead:lead + 3001]
+            h = ZeroGrads([g], out=out)
+            for call in (lambda: h.zero_grads_scale(2.0), lambda: h.zero_grads_clip_norm(1e-3, inv_loss_scale=2.0)):
+                out.zero_()
+                call()
+                assert (bits(out) == bits(emulate(g, 2.0, 1.0, dst))).all()
+                assert (bits(out)[[0, 1, 500, 1501, 3000]] == canonical).all()
+
+
 def test_extremes_of_fp32():
     """Squares beyond fp32's range at both ends; fp16 results beyond its range become infinite."""
     big = torch.full((5000,), 3e38, device="cuda")
@@ -394,6 +417,8 @@ def test_refusals_of_calls():
         ZeroGrads([g], out=torch.zeros(99, device="cuda"))
     with pytest.raises(ValueError):
         ZeroGrads([g], out=[])
+    with pytest.raises(ValueError, match="tensor 1"):
+        ZeroGrads([g, None])
     for bad in ([], [g, g], [g[:99]], [g.half()], [torch.zeros(100)]):
         with pytest.raises((ValueError, IndexError)):
             h.zero_grads_bind(bad)

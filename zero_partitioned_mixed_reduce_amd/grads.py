@@ -144,6 +144,9 @@ class ZeroGrads:
 
     def _check(self, tensors, out):
         """Checks a list and returns its destinations, one per tensor (None: in place)."""
+        for i, t in enumerate([*tensors, *(out if isinstance(out, (list, tuple)) else [])]):
+            if not isinstance(t, torch.Tensor):
+                raise ValueError(f"tensor {i} of the list is {type(t).__name__}, not a tensor")
         dev = tensors[0].device
         for i, t in enumerate(tensors):
             if t.device.type != "cuda" or t.device != dev:
