@@ -170,7 +170,9 @@ def check(fn, status):
 
 
 def _call(name, *args):
-    check(name, getattr(lib(), name)(*args))
+    status = getattr(_lib or lib(), name)(*args)
+    if status != ZERO_OK:
+        raise ZeroError(name, status)
 
 
 def zero_shard_plan(desc):

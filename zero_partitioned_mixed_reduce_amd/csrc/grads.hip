@@ -20,10 +20,12 @@
 #include "zs_internal.h"
 
 // Tuning knobs (each set to the value measured fastest on MI355X):
-//   ZS_GRADS_NORM_U   groups per lane in flight in the norm kernel; 1 and 4 measured 0-2% slower
-//                     on lists beyond the Infinity Cache and 4-25% on shorter ones, 8 10% slower
+//   ZS_GRADS_NORM_U   groups per lane in flight in the norm kernel: 4 measured 0-4% slower, 1 as
+//                     fast on 1.56e9 elements and 38% slower on 1.2e8 (70 us for 51)
 //   ZS_GRADS_NT_BYTES a norm over a list of more bytes than this (the Infinity Cache) reads it
-//                     with non-temporal loads (1.6 GB of fp32 4-8% faster, bf16 3%)
+//                     with non-temporal loads: 1.56e9 bf16 elements 495 us and 533 without, 4.1e8
+//                     fp32 263 and 292.  Shorter lists stay cached for the clip that follows
+//                     (1.2e7 to 1e8 bf16 elements are clipped 2-5% faster without)
 #ifndef ZS_GRADS_NORM_U
 #define ZS_GRADS_NORM_U 2
 #endif
