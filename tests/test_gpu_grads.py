@@ -464,6 +464,50 @@ def test_bind(count):
     assert (bits(big[seed:seed + total]) == bits(torch.cat([emulate(g, 1.0, 1.0, torch.float32) for g in moved]))).all()
 
 
+def test_bind_with_empty_tensors():
+    """Empty tensors have no address of their own, planned and bound: flat, per-tensor and in-place destinations."""
+    def make(v):
+        return [torch.full((300,), v, device="cuda"), torch.empty(0, device="cuda"), torch.full((2000,), v, device="cuda"),
+                torch.empty((4, 0), device="cuda")]
+
+    for mode in ("flat", "list", "in place"):
+        def out():
+            return (torch.zeros(2300, device="cuda") if mode == "flat" else None if mode == "in place"
+                    else [torch.zeros_like(g) for g in make(0.0)])
+        h = ZeroGrads(make(1.0), out=out())
+        h.zero_grads_scale(2.0)
+        grads, o = make(3.0), out()
+        h.zero_grads_bind(grads, *([] if o is None else [o]))
+        h.zero_grads_norm(per_tensor=True)
+        assert h.tensor_acc.tolist() == [2700.0, 0.0, 18000.0, 0.0]
+        h.zero_grads_scale(2.0)
+        got = grads if o is None else o if isinstance(o, list) else [o]
+        assert all((t == 6.0).all() for t in got)
+
+
+@pytest.mark.parametrize("dst", DT)
+@pytest.mark.parametrize("src", DT)
+def test_all_magnitudes(src, dst):
+    """Random bit patterns, subnormals, infinities and NaNs among them: every product and conversion rounds as on the
+    CPU."""
+    n = 70_001
+    g = torch.Generator().manual_seed(5)
+    if src == torch.float32:
+        raw = torch.randint(-2 ** 31, 2 ** 31, (n,), generator=g).to(torch.int32)
+    else:
+        raw = torch.randint(-2 ** 15, 2 ** 15, (n,), generator=g).to(torch.int16)
+    x = raw.view(src).cuda()
+    assert int(torch.isnan(x).sum()) > 100
+    out = torch.empty(n + 1, dtype=dst, device="cuda")[1:]
+    h = ZeroGrads([x], out=out)
+    for f in (1.0, 0.7, 2.0 ** -20, 2.0 ** 30):
+        h.zero_grads_scale(f)
+        want = emulate(x, f, 1.0, dst)
+        nan = torch.isnan(want).numpy()
+        same = bits(out) == bits(want)
+        assert (same | (nan if dst == torch.float32 else False)).all() and torch.isnan(out.cpu()).numpy()[nan].all()
+
+
 def test_exchange_on_the_host_and_on_the_device():
     """Two ranks' halves of a list clip like the whole list, with the statistics exchanged either way."""
     grads = ragged(4, 20, 9000, [torch.float32])

@@ -115,6 +115,21 @@ def test_overlap_rules():
     refused(cut[0], entry(src=BASE + 2 * 40, dst=BASE + 2 * 40, rows=16, cols=40, sp=240, dp=240), needle="overlaps")
 
 
+def test_overlap_rules_stay_fast():
+    """A list that repeats one tensor many times is planned without comparing every pair."""
+    import time
+    n = 200_000
+    t = listof(*[entry(cols=64)] * n)
+    began = time.monotonic()
+    assert zpm.zero_grads_plan(t).elems == 64 * n
+    assert time.monotonic() - began < 5.0
+    u = listof(*[entry(cols=64, dst=BASE + (1 << 40) + 128 * i) for i in range(n)])
+    u[n - 1].dst = BASE + (1 << 40)            # out of order, so every pair of neighbours is compared
+    with pytest.raises(zpm.ZeroError):
+        zpm.zero_grads_plan(u)
+    assert time.monotonic() - began < 10.0
+
+
 def elements_of(t, dst=False):
     """Byte offsets from the tensor's first element, in list order."""
     es = 4 if (t.dst_dtype if dst else t.src_dtype) == F32 else 2

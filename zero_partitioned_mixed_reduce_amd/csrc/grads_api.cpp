@@ -114,6 +114,7 @@ zero_status_t bind(zero_grads_t h, void* const* src, void* const* dst, hipStream
   std::vector<zero_grads_tensor_t> t = h->plan.tensors;
   const int64_t n = (int64_t)t.size();
   for (int64_t i = 0; i < n; ++i) {
+    if (t[i].rows * t[i].cols == 0) continue;  // has no address
     t[i].src = src[i];
     if (h->plan.in_place[i]) {
       if (dst && dst[i] && dst[i] != src[i])

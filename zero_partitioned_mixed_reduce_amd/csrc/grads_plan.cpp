@@ -104,8 +104,7 @@ zero_status_t check_grads_addresses(const std::vector<zero_grads_tensor_t>& t, c
   }
   // destinations in ascending order apart from every source, as in a flat buffer
   if (!any_in_place && ordered && (!any_dst || dst_hi <= src_lo || src_hi <= dst_lo)) return ZERO_OK;
-  // Any order: sweep over all spans by address.  A destination is compared with every span it
-  // interleaves with; what is only read is free to repeat.
+  // Any order: sweep over all spans by address.
   std::vector<Span> all;
   for (int64_t i = 0; i < n; ++i) {
     if (t[i].rows * t[i].cols == 0) continue;
@@ -116,20 +115,30 @@ zero_status_t check_grads_addresses(const std::vector<zero_grads_tensor_t>& t, c
     all.back().written = 2;
   }
   std::sort(all.begin(), all.end(), [](const Span& a, const Span& b) { return a.begin < b.begin; });
-  std::vector<Span> open;
+  // The spans that reach beyond the present one's begin, read and written ones apart: two that
+  // are only read are not compared.  Once tensors without a destination have been found to
+  // overlap, they count as read, and only destinations are looked for.
+  std::vector<Span> open[2];
   for (const Span& s : all) {
-    size_t keep = 0;
-    for (const Span& o : open) {
-      if (o.end <= s.begin) continue;
-      if ((o.written || s.written) && share(o, s)) {
-        const Span& d = s.written > o.written ? s : o;
-        if (d.written == 2) return bad(err, d.tensor, "destination overlaps a source or another destination");
-        *overlap = d.tensor;
+    for (int w = s.written && !(s.written == 1 && *overlap >= 0) ? 0 : 1; w < 2; ++w) {
+      size_t keep = 0;
+      for (const Span& o : open[w]) {
+        if (o.end <= s.begin) continue;
+        if (share(o, s)) {
+          const Span& d = s.written > o.written ? s : o;
+          if (d.written == 2) return bad(err, d.tensor, "destination overlaps a source or another destination");
+          *overlap = d.tensor;
+        }
+        open[w][keep++] = o;
       }
-      open[keep++] = o;
+      open[w].resize(keep);
     }
-    open.resize(keep);
-    open.push_back(s);
+    if (*overlap >= 0 && !open[1].empty()) {
+      auto given = std::stable_partition(open[1].begin(), open[1].end(), [](const Span& o) { return o.written == 2; });
+      open[0].insert(open[0].end(), given, open[1].end());
+      open[1].erase(given, open[1].end());
+    }
+    open[s.written == 2 || (s.written == 1 && *overlap < 0)].push_back(s);
   }
   return ZERO_OK;
 }

@@ -40,6 +40,8 @@ def describe(i, src, dst):
         raise ValueError(f"tensor {i}: need a dense float16, bfloat16 or float32 tensor, got {src.dtype}, {src.layout}")
     if dst is not None and (dst.layout is not torch.strided or dst.dtype not in _DT):
         raise ValueError(f"out {i}: need a dense float16, bfloat16 or float32 tensor, got {dst.dtype}, {dst.layout}")
+    if src.is_neg() or (dst is not None and dst.is_neg()):
+        raise ValueError(f"tensor {i}: a lazily negated view; resolve_neg() it first")
     if dst is not None and dst.numel() != src.numel():
         raise ValueError(f"out {i} has {dst.numel()} elements, tensor {i} has {src.numel()}")
     t = abi.zero_grads_tensor_t()
@@ -104,6 +106,8 @@ class ZeroGrads:
 
     After a norm, `norm` (0-dim) and, with per_tensor, `norms` [n] are fp32 device tensors in the workspace,
     `found_inf` (int32), `acc` and `tensor_acc` (fp64) likewise; they hold the handle's latest results.
+
+    Results in place are written behind autograd's back, as into detached tensors.
 
     Calls use the current stream of the tensors' device, and the handle keeps the tensors alive until it is bound
     to others or closed.  As with any torch call, tensors used on another stream than the one they were allocated
