@@ -646,11 +646,13 @@ def test_two_handles_at_once():
 
 
 def test_closed_handle_and_kept_tensors():
-    h = ZeroGrads([torch.ones(5000, device="cuda") for _ in range(3)])   # only the handle keeps them
-    for _ in range(4):
-        torch.zeros(5000, device="cuda")
+    h = ZeroGrads((torch.ones(5000, device="cuda") for _ in range(3)),   # only the handle keeps them
+                  out=(torch.zeros(5000, device="cuda") for _ in range(3)))
+    rest = [torch.full((5000,), 5.0, device="cuda") for _ in range(8)]
     h.zero_grads_norm()
     assert float(h.acc) == 15000.0
+    h.zero_grads_scale(2.0)
+    assert all((o == 2).all() for o in h._out) and all((r == 5).all() for r in rest)
     h.close()
     h.close()
     for call in (h.zero_grads_norm, h.query, lambda: h.zero_grads_scale(1.0), lambda: h.zero_grads_clip_norm(1.0)):

@@ -110,13 +110,16 @@ class ZeroGrads:
     Results in place are written behind autograd's back, as into detached tensors.
 
     Calls use the current stream of the tensors' device, and the handle keeps the tensors alive until it is bound
-    to others or closed.  As with any torch call, tensors used on another stream than the one they were allocated
-    on must be kept until that stream is done with them."""
+    to others or closed; a captured graph needs the handle, whose workspace it uses.  As with any torch call,
+    tensors used on another stream than the one they were allocated on must be kept until that stream is done
+    with them."""
 
     def __init__(self, tensors, out=None):
         self._tensors = list(tensors)
         if not self._tensors:
             raise ValueError("an empty list")
+        if out is not None and not isinstance(out, torch.Tensor):
+            out = list(out)
         self._in_place = out is None
         dsts = self._check(self._tensors, out)
         self._out = out
@@ -148,7 +151,7 @@ class ZeroGrads:
 
     def _check(self, tensors, out):
         """Checks a list and returns its destinations, one per tensor (None: in place)."""
-        for i, t in enumerate([*tensors, *(out if isinstance(out, (list, tuple)) else [])]):
+        for i, t in enumerate([*tensors, *(out if isinstance(out, list) else [])]):
             if not isinstance(t, torch.Tensor):
                 raise ValueError(f"tensor {i} of the list is {type(t).__name__}, not a tensor")
         dev = tensors[0].device
@@ -167,7 +170,7 @@ class ZeroGrads:
                 dsts.append(out[at:at + t.numel()])
                 at += t.numel()
         else:
-            dsts = list(out)
+            dsts = out
             if len(dsts) != len(tensors):
                 raise ValueError(f"{len(tensors)} tensors, {len(dsts)} out tensors")
         for i, t in enumerate(dsts):
