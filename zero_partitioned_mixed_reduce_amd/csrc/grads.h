@@ -27,6 +27,11 @@ constexpr int kGradsWaves = kGradsBlock / 64;
 constexpr int kGradsRun = 4;
 // Items of one tensor whose results a wave joins at once.
 constexpr int kGradsJoin = 64;
+// Results that one wave joins without their groups' (see join_level).
+#ifndef ZS_GRADS_DIRECT
+#define ZS_GRADS_DIRECT 1024
+#endif
+constexpr int kGradsDirect = ZS_GRADS_DIRECT;
 // Limit of the blocks of work (each up to four blocks of a launch, whose limit is 2^32 - 1
 // threads) and of the tensors.
 constexpr int64_t kGradsMaxBlocks = (1 << 22) - 1;

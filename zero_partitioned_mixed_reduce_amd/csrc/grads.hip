@@ -399,12 +399,53 @@ __device__ __forceinline__ uint32_t arrive(uint64_t* part, typename A::V v, uint
 __device__ __forceinline__ void rearm(uint32_t* count) {
   __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-// The join of p[0 .. n) by one wave: ascending per lane, then a butterfly.
+// The join of p[0 .. n) by one wave: ascending per lane, then a butterfly.  Beyond one result
+// per lane eight loads are in flight (a load that is not needed repeats the last).
 template <class A>
 __device__ __forceinline__ typename A::V wave_join_of(const uint64_t* p, uint32_t n) {
+  constexpr uint32_t kFlight = 8;
+  const uint32_t lane = threadIdx.x & 63;
   typename A::V v = A::none();
-  for (uint32_t i = threadIdx.x & 63; i < n; i += 64) v = A::join(v, A::load(p + i));
+  if (n <= 64) {
+    if (lane < n) v = A::load(p + lane);
+    return wave_join<A>(v);
+  }
+  for (uint32_t i0 = 0; i0 < n; i0 += 64 * kFlight) {
+    typename A::V x[kFlight];
+#pragma unroll
+    for (uint32_t k = 0; k < kFlight; ++k) {
+      const uint32_t i = i0 + 64 * k + lane;
+      x[k] = A::load(p + (i < n ? i : n - 1));
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < kFlight; ++k) v = A::join(v, i0 + 64 * k + lane < n ? x[k] : A::none());
+  }
   return wave_join<A>(v);
+}
+
+// Two levels above n results in groups, by the wave that found its group complete: whether it
+// is the last of all, and then their join in *v.  Up to kGradsDirect results the group only
+// arrives at the top, and the last one joins all of them at once; beyond, it leaves its own
+// join.  (1e6 to 4.2e6 bf16 elements, 130 to 520 blocks: 5.7 to 6.6 us, and 6.4 to 7.0 with
+// every group's join stored; 1000 small tensors the same either way.)
+template <class A>
+__device__ __forceinline__ bool join_level(uint32_t n, uint32_t groups, const uint64_t* part, uint32_t first,
+                                           uint32_t size, uint64_t* gpart, uint32_t g, uint32_t* top,
+                                           typename A::V* v) {
+  const bool lead = (threadIdx.x & 63) == 0;
+  const bool direct = n <= (uint32_t)kGradsDirect;
+  uint32_t had = 0;
+  if (!direct) *v = wave_join_of<A>(part + first, size);
+  if (groups > 1) {
+    if (lead)
+      had = direct ? __hip_atomic_fetch_add(top, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+                   : arrive<A>(gpart + g, *v, top);
+    if (__shfl(had, 0, 64) + 1 != groups) return false;
+    if (lead) rearm(top);
+    if (!direct) *v = wave_join_of<A>(gpart, groups);
+  }
+  if (direct) *v = wave_join_of<A>(part, n);
+  return true;
 }
 
 // What the end of a norm block knows of one of its items.
@@ -454,30 +495,18 @@ __device__ void norm_block_end(typename Acc<KIND>::V item, int n_items, int firs
     const int tensor = __shfl(e.tensor, j, 64), first = __shfl(e.first, j, 64), items = __shfl(e.count, j, 64);
     const int join = __shfl(e.join, j, 64);
     const uint32_t jg = __shfl(jgroup, j, 64), n = __shfl(jsize, j, 64);
-    typename A::V t = wave_join_of<A>(a.item_part + first + jg * kGradsJoin, n);
     if (lane == 0) rearm(a.join_count + 16 * (int64_t)(join + (int)jg));
     const uint32_t groups = ((uint32_t)items + kGradsJoin - 1) / kGradsJoin;
-    if (groups > 1) {
-      uint32_t* top = a.join_count + 16 * (int64_t)(join + (int)groups);
-      uint32_t had = 0;
-      if (lane == 0) had = arrive<A>(a.join_part + join + jg, t, top);
-      if (__shfl(had, 0, 64) + 1 != groups) continue;
-      t = wave_join_of<A>(a.join_part + join, groups);
-      if (lane == 0) rearm(top);
-    }
-    if (lane == 0) finish_tensor<KIND>(t, tensor, a, clip);
+    typename A::V t;
+    if (join_level<A>((uint32_t)items, groups, a.item_part + first, jg * kGradsJoin, n, a.join_part + join, jg,
+                      a.join_count + 16 * (int64_t)(join + (int)groups), &t) &&
+        lane == 0)
+      finish_tensor<KIND>(t, tensor, a, clip);
   }
   if (__shfl(before, 63, 64) + 1 != gsize) return;
-  v = wave_join_of<A>(a.part + g0, gsize);
   if (lane == 0) rearm(a.gcount + 16 * g);
-  if (ngroups > 1) {
-    uint32_t had = 0;
-    if (lane == 0) had = arrive<A>(a.gpart + g, v, &a.sc->counter);
-    if (__shfl(had, 0, 64) + 1 != ngroups) return;
-    v = wave_join_of<A>(a.gpart, ngroups);
-    if (lane == 0) rearm(&a.sc->counter);
-  }
-  if (lane == 0) finish_list<KIND>(v, a.sc, clip);
+  if (join_level<A>(nb, ngroups, a.part, g0, gsize, a.gpart, g, &a.sc->counter, &v) && lane == 0)
+    finish_list<KIND>(v, a.sc, clip);
 }
 
 // A block takes a.run consecutive block items, so that what ends a block -- its sum, a store, an
