@@ -331,7 +331,9 @@ def ragged(seed, count, top, dtypes=DT):
     return [rand(seed * 1000 + i, int(r.randint(1, top)), dtypes[r.randint(len(dtypes))]) for i in range(count)]
 
 
-@pytest.mark.parametrize("count,top", [(1, 3_000_000), (40, 60_000), (900, 3000), (5000, 40), (300, 1100)])
+# beside the many small ones: more than 1024 blocks, and (of one tensor of 1.4e8 elements) runs of items
+@pytest.mark.parametrize("count,top", [(1, 3_000_000), (40, 60_000), (900, 3000), (5000, 40), (300, 1100),
+                                       (3, 24_000_000), (1, 150_000_000)])
 def test_many_tensors_and_same_bits(count, top):
     """Mixed types and sizes: against the formula; the same bits from every repetition, from the two calls and the
     one, and with other work on the GPU."""
