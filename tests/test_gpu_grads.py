@@ -360,6 +360,25 @@ def test_many_tensors_and_same_bits(count, top):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("kind", [L2, MAX])
+@pytest.mark.parametrize("rows,cols,at,width,lone", [(21000, 4010, 3, 4001, 0), (2300, 30013, 5, 29999, 3), (1, 1, 0, 1, 6000)])
+def test_long_lists_of_pieces(kind, rows, cols, at, width, lone):
+    """Lists of more than 8192 blocks of work, whose blocks take several items: rows shorter and longer than one,
+    odd starts, and tensors of one to four items that begin and end inside a block's share."""
+    base = rand(rows, (rows, cols), torch.bfloat16)
+    grads = ragged(rows, 40, 30_000) + [base[:, at:at + width]] + ragged(lone, lone, 30_000)
+    h = ZeroGrads(grads, out=torch.empty(sum(g.numel() for g in grads), dtype=torch.float32, device="cuda"))
+    for _ in range(3):
+        h.zero_grads_norm(kind, per_tensor=True)
+        check_norms(h, grads, kind, 1.0)
+    whole, each = h.acc.clone(), h.norms.clone()
+    h.zero_grads_norm(kind)
+    assert torch.equal(h.acc, whole)
+    grads[-1][(-1,) * grads[-1].dim()] = float("inf")
+    h.zero_grads_norm(kind, per_tensor=True)
+    assert int(h.found_inf) == 1 and torch.isinf(h.norms[-1]) and torch.equal(h.norms[:-1], each[:-1])
+
+
 def test_order_of_calls():
     grads = [rand(1, 100, torch.float32)]
     h = ZeroGrads(grads)

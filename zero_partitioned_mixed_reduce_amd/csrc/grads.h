@@ -25,6 +25,16 @@ constexpr int kGradsBlock = 256;
 constexpr int kGradsWaves = kGradsBlock / 64;
 // Consecutive block items that a block of the norm kernel takes at most.
 constexpr int kGradsRun = 4;
+// Bytes from one arrival counter to the next.  An arrival is done by the memory, and while many
+// of them meet in a few channels the reads of those channels wait: with counters 64 bytes apart
+// in groups of 256 blocks the norm of 1.56e9 bf16 elements takes 498 us, with 256 bytes 467, in
+// groups of 64 blocks 461; without any arrival the reads take 446.  512, 1024 and 4096 bytes
+// measured the same as 256.
+#ifndef ZS_GRADS_PITCH
+#define ZS_GRADS_PITCH 256
+#endif
+constexpr int kGradsPitch = ZS_GRADS_PITCH;
+static_assert(kGradsPitch % 64 == 0, "counters on lines of their own");
 // Items of one tensor whose results a wave joins at once.
 constexpr int kGradsJoin = 64;
 // Results that one wave joins without their groups' (see join_level).
@@ -129,9 +139,9 @@ struct GradsArgs {
   float* coefs;          // of the last clip by each tensor's norm
   uint64_t* part;        // one per block of the norm kernel
   uint64_t* item_part;   // one per item
-  uint32_t* gcount;      // one 64-byte line per group of blocks
+  uint32_t* gcount;      // one per group of blocks, kGradsPitch bytes apart
   uint64_t* gpart;       // one per group of blocks
-  uint32_t* join_count;  // one 64-byte line per kGradsJoin items of a tensor, and one more per tensor of several
+  uint32_t* join_count;  // one per kGradsJoin items of a tensor, and one more per tensor of several; likewise
   uint64_t* join_part;   // beside them
   int64_t bytes_in;      // of the sources
   int32_t n_block_items, n_chunks, n_blocks, n_tensors;

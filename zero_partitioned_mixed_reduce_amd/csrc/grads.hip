@@ -9,7 +9,7 @@
 // (global loads take any), so tensors that lie back to back at odd offsets need no slow path.
 //
 // Measured (MI355X; a copy reaches 6.4 TB/s, pure reads 7.1): norm of 1.56e9 bf16 elements
-// 495 us, 6.3 TB/s; scaling them into another buffer 1012 us, 6.1 TB/s, and 4.1e8 fp32
+// 478 us, 6.5 TB/s; scaling them into another buffer 1012 us, 6.1 TB/s, and 4.1e8 fp32
 // elements into bf16 361 us, 6.7 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -20,14 +20,14 @@
 #include "zs_internal.h"
 
 // Tuning knobs (each set to the value measured fastest on MI355X):
-//   ZS_GRADS_NORM_U   groups per lane in flight in the norm kernel: 4 measured 0-4% slower, 1 as
-//                     fast on 1.56e9 elements and 38% slower on 1.2e8 (70 us for 51)
+//   ZS_GRADS_NORM_U   groups per lane in flight in the norm kernel: 2 measured the same, and 2%
+//                     slower in clips of 1.2e8 elements, 8 is 3-5% slower
 //   ZS_GRADS_NT_BYTES a norm over a list of more bytes than this (the Infinity Cache) reads it
-//                     with non-temporal loads: 1.56e9 bf16 elements 495 us and 533 without, 4.1e8
-//                     fp32 263 and 292.  Shorter lists stay cached for the clip that follows
+//                     with non-temporal loads: 1.56e9 bf16 elements 478 us and 536 without; 4.1e8
+//                     fp32 clipped in 608 and 640.  Shorter ones stay cached for the clip behind
 //                     (1.2e7 to 1e8 bf16 elements are clipped 2-5% faster without)
 #ifndef ZS_GRADS_NORM_U
-#define ZS_GRADS_NORM_U 2
+#define ZS_GRADS_NORM_U 4
 #endif
 #ifndef ZS_GRADS_NT_BYTES
 #define ZS_GRADS_NT_BYTES (256ll << 20)
@@ -458,7 +458,8 @@ struct ItemEnd {
 // atomics: the block arrives on its group's counter, the group's last block joins the group's
 // results, and the last group joins the groups'.  With per_tensor every item's result joins
 // its tensor's in the same way, in groups of kGradsJoin items; a tensor of one item is
-// finished at once.  All arrivals of a block are counted together, one per lane.  Counters are
+// finished at once.  All arrivals of a block are counted together, one per lane; items that share
+// a counter arrive as one (their stores are the same wave's, complete before it).  Counters are
 // re-armed by their last arrival.
 template <int KIND>
 __device__ void norm_block_end(typename Acc<KIND>::V item, int n_items, int first_item, const ItemEnd* ends,
@@ -473,7 +474,7 @@ __device__ void norm_block_end(typename Acc<KIND>::V item, int n_items, int firs
   const uint32_t ngroups = (nb + group - 1) / group;
   ItemEnd e = {0, 0, 0, 0};
   uint64_t* part = a.part + b;
-  uint32_t* count = a.gcount + 16 * g;
+  uint32_t* count = a.gcount + kGradsPitch / 4 * g;
   uint32_t jsize = 0, jgroup = 0;
   if (per_tensor && lane < n_items) {
     e = ends[lane];
@@ -482,38 +483,46 @@ __device__ void norm_block_end(typename Acc<KIND>::V item, int n_items, int firs
     jsize = (uint32_t)e.count - jgroup * kGradsJoin;
     if (jsize > (uint32_t)kGradsJoin) jsize = kGradsJoin;
     part = a.item_part + first_item + lane;
-    count = a.join_count + 16 * (int64_t)(e.join + (int)jgroup);
+    count = a.join_count + kGradsPitch / 4 * (int64_t)(e.join + (int)jgroup);
     if (e.count == 1) finish_tensor<KIND>(item, e.tensor, a, clip);
   }
-  uint32_t before = 0;
+  const int at = e.count > 1 ? e.join + (int)jgroup : -1;
+  const int left = __shfl_up(at, 1, 64);
   const bool own = lane == 63;  // the lane that arrives for the block
-  if (own || e.count > 1) before = arrive<A>(part, own ? v : item, count);
-  uint64_t last = __ballot(e.count > 1 && before + 1 == jsize);
+  const bool leads = at >= 0 && (lane == 0 || left != at);
+  const uint64_t same = ~__ballot(at >= 0 && !leads) >> lane >> 1;  // bit 0: the next lane is not of this arrival
+  const uint32_t weight = own ? 1 : 1 + (uint32_t)__builtin_ctzll(same);
+  if (own || at >= 0) A::store(part, own ? v : item);
+  stores_complete();
+  uint32_t before = 0;
+  if (own || leads) before = __hip_atomic_fetch_add(count, weight, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  uint64_t last = __ballot(leads && before + weight == jsize);
   while (last) {
     const int j = __builtin_ctzll(last);
     last &= last - 1;
     const int tensor = __shfl(e.tensor, j, 64), first = __shfl(e.first, j, 64), items = __shfl(e.count, j, 64);
     const int join = __shfl(e.join, j, 64);
     const uint32_t jg = __shfl(jgroup, j, 64), n = __shfl(jsize, j, 64);
-    if (lane == 0) rearm(a.join_count + 16 * (int64_t)(join + (int)jg));
+    if (lane == 0) rearm(a.join_count + kGradsPitch / 4 * (int64_t)(join + (int)jg));
     const uint32_t groups = ((uint32_t)items + kGradsJoin - 1) / kGradsJoin;
     typename A::V t;
     if (join_level<A>((uint32_t)items, groups, a.item_part + first, jg * kGradsJoin, n, a.join_part + join, jg,
-                      a.join_count + 16 * (int64_t)(join + (int)groups), &t) &&
+                      a.join_count + kGradsPitch / 4 * (int64_t)(join + (int)groups), &t) &&
         lane == 0)
       finish_tensor<KIND>(t, tensor, a, clip);
   }
   if (__shfl(before, 63, 64) + 1 != gsize) return;
-  if (lane == 0) rearm(a.gcount + 16 * g);
+  if (lane == 0) rearm(a.gcount + kGradsPitch / 4 * g);
   if (join_level<A>(nb, ngroups, a.part, g0, gsize, a.gpart, g, &a.sc->counter, &v) && lane == 0)
     finish_list<KIND>(v, a.sc, clip);
 }
 
 // A block takes a.run consecutive block items, so that what ends a block -- its sum, a store, an
-// arrival -- is paid once for them, or a wave item per wave.  The next item's table entry is
-// requested before the present item is streamed.  Only the first wave stays for the end; the
-// others leave their places to the blocks that wait.  1.56e9 bf16 elements take 734 us in runs
-// of one item, 620 of 2, 495 of 4, 8 and 16; 1.2e8 take 70, 59, 52, 54 and 55.
+// arrival -- is paid once for them, or a wave item per wave.  Items that go on with one run of
+// elements are streamed as one; the first of them has their sum, the others nothing.  Only the
+// first wave stays for the end; the others leave their places to the blocks that wait.  The norm
+// of 1.56e9 bf16 elements takes 524 us in runs of one item, 488 of 2, 477 of 4, 473 of 8 and 470
+// of 16; the clip of 1.2e8 124, 124, 124, 134 and 129 (few blocks, and the last ones alone).
 template <int KIND, bool NT>
 __global__ void __launch_bounds__(kGradsBlock, 7) grads_norm_kernel(GradsArgs a, float inv, int per_tensor,
                                                                  ClipArgs clip) {
@@ -528,14 +537,25 @@ __global__ void __launch_bounds__(kGradsBlock, 7) grads_norm_kernel(GradsArgs a,
   if (b < runs) {
     first = b * a.run;
     n_items = a.n_block_items - first < a.run ? a.n_block_items - first : a.run;
-    GradsChunk k = entry(a.chunks + first);
-    for (int j = 0;; ++j) {
-      const GradsChunk next = entry(a.chunks + first + (j + 1 < n_items ? j + 1 : j));
+    for (int j = 0; j < n_items;) {
+      GradsChunk k = entry(a.chunks + first + j);
+      int m = 1;
+      if (a.run > 1) {  // all entries are requested together
+        bool on = true;
+#pragma unroll
+        for (int i = 1; i < kGradsRun; ++i) {
+          const GradsChunk* c = a.chunks + first + (j + i < n_items ? j + i : n_items - 1);
+          const int cols = c->cols, before = c->before, after = c->after;
+          on = on && j + i < n_items && before != 0;
+          k.cols += on ? cols : 0;
+          k.after = on ? (int16_t)after : k.after;
+          m += on;
+        }
+      }
       const typename A::V x = wave_join<A>(norm_item<KIND, NT, kGradsBlock>(k, inv, (int)threadIdx.x));
-      if (lane == 0) sums[j][wave] = x;
-      if (threadIdx.x == 0) ends[j] = ItemEnd{k.tensor, k.first, k.count, k.join};
-      if (j + 1 >= n_items) break;
-      k = next;
+      if (lane < m) sums[j + lane][wave] = lane == 0 ? x : A::none();
+      if ((int)threadIdx.x < m) ends[j + threadIdx.x] = ItemEnd{k.tensor, k.first, k.count, k.join};
+      j += m;
     }
     __syncthreads();
     if (wave != 0) return;

@@ -226,12 +226,13 @@ zero_status_t build_grads_plan(const zero_grads_tensor_t* tensors, int64_t n, Gr
   p.n_blocks = n_blocks;
   p.run = n_block >= kGradsRunFrom ? kGradsRun : 1;
   p.norm_grid = (n_block + p.run - 1) / p.run + n_wave_blocks;
-  // Groups of about the square root of the blocks: every arrival on one counter takes about
-  // 10 ns, so groups of 256 made the norm of 4.2e6 bf16 elements (512 blocks) 9.1 us, groups of
-  // 64 6.7.  Up to 128 blocks one group is as fast as a second level.
+  // Groups of about the square root of the blocks, at most 64: every arrival on one counter
+  // takes about 10 ns, so groups of 256 made the norm of 4.2e6 bf16 elements (512 blocks) 9.1 us,
+  // groups of 64 6.7.  1.56e9 elements take 467 us in groups of 256, 461 of 64, 506 of 16, whose
+  // own arrivals crowd the top.  Up to 128 blocks one group is as fast as a second level.
   p.group = 128;
   if (p.norm_grid > 128)
-    for (p.group = 16; p.group < 256 && p.group * p.group < p.norm_grid;) p.group *= 2;
+    for (p.group = 16; p.group < 64 && p.group * p.group < p.norm_grid;) p.group *= 2;
   const int64_t n_groups = (p.norm_grid + p.group - 1) / p.group;
   p.info.num_chunks = n_block + n_wave;
   auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
@@ -247,8 +248,8 @@ zero_status_t build_grads_plan(const zero_grads_tensor_t* tensors, int64_t n, Gr
   l.gpart = up(l.item_part + 8 * p.info.num_chunks);
   l.join_part = up(l.gpart + 8 * n_groups);
   l.gcount = up(l.join_part + 8 * p.n_joins);
-  l.join_count = up(l.gcount + 64 * n_groups);
-  l.end = up(l.join_count + 64 * p.n_joins);
+  l.join_count = up(l.gcount + kGradsPitch * n_groups);
+  l.end = up(l.join_count + kGradsPitch * p.n_joins);
   p.info.workspace_bytes = l.end;
   *out = std::move(p);
   return ZERO_OK;
