@@ -119,7 +119,7 @@ zero_status_t zero_grads_norm(zero_grads_t h, int32_t norm, float inv_loss_scale
  * tensor_acc: sum for L2, maximum for MAX; found_inf: maximum).  norm and
  * norms [n] are the norms in fp32; after a zero_grads_clip, norm is the one it
  * clipped by.  tensor_acc and norms are written by calls with per_tensor (an
- * empty tensor's are 0).  Any output pointer may be NULL. */
+ * empty tensor's are 0 in each of them).  Any output pointer may be NULL. */
 zero_status_t zero_grads_device(zero_grads_t h, double** acc, int32_t** found_inf, float** norm, double** tensor_acc,
                                 float** norms);
 

@@ -107,6 +107,7 @@ struct GradsPlan {
   int64_t group;          // blocks of the norm kernel whose results one group joins
   int64_t n_joins;        // counters of the tensors of several items
   int64_t bytes_in;       // of the sources
+  int64_t n_empty;        // tensors without elements
   bool all16;             // every source and destination is 16-bit
   GradsLayout layout;
 };
@@ -133,6 +134,7 @@ struct GradsBindArgs {
 
 struct GradsArgs {
   const GradsChunk* chunks;
+  const GradsRange* ranges;
   GradsScalars* sc;
   double* tensor_acc;
   float* norms;
@@ -144,7 +146,7 @@ struct GradsArgs {
   uint32_t* join_count;  // one per kGradsJoin items of a tensor, and one more per tensor of several; likewise
   uint64_t* join_part;   // beside them
   int64_t bytes_in;      // of the sources
-  int32_t n_block_items, n_chunks, n_blocks, n_tensors;
+  int32_t n_block_items, n_chunks, n_blocks, n_tensors, n_empty;
   int32_t run, group;
   int32_t all16;         // every source and destination is 16-bit
 };

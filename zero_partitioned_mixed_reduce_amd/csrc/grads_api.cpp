@@ -54,6 +54,7 @@ zero_status_t init(const zero_grads_tensor_t* tensors, int64_t n, void* workspac
   char* ws = static_cast<char*>(workspace);
   zs::GradsArgs a;
   a.chunks = reinterpret_cast<zs::GradsChunk*>(ws + p.layout.chunks);
+  a.ranges = reinterpret_cast<zs::GradsRange*>(ws + p.layout.ranges);
   a.sc = reinterpret_cast<zs::GradsScalars*>(ws);
   a.tensor_acc = reinterpret_cast<double*>(ws + p.layout.tensor_acc);
   a.norms = reinterpret_cast<float*>(ws + p.layout.norms);
@@ -69,6 +70,7 @@ zero_status_t init(const zero_grads_tensor_t* tensors, int64_t n, void* workspac
   a.n_chunks = (int32_t)p.info.num_chunks;
   a.n_blocks = (int32_t)p.n_blocks;
   a.n_tensors = (int32_t)n;
+  a.n_empty = (int32_t)p.n_empty;
   a.run = (int32_t)p.run;
   a.group = (int32_t)p.group;
   a.all16 = p.all16;
@@ -85,7 +87,7 @@ zero_status_t init(const zero_grads_tensor_t* tensors, int64_t n, void* workspac
   else if ((e = hipMemcpyAsync(ws + p.layout.ranges, p.ranges.data(), p.ranges.size() * sizeof(zs::GradsRange),
                                hipMemcpyHostToDevice, st)) != hipSuccess)
     rs = hip_fail("hipMemcpyAsync(tensor table)", e);
-  // the counters start at zero (and are re-armed by every pass); empty tensors' norms stay zero
+  // the counters start at zero (and are re-armed by every pass), the tensors' results until a first pass too
   else if ((e = zs::launch_fill_zero(reinterpret_cast<float*>(a.tensor_acc),
                                      (p.layout.part - p.layout.tensor_acc) / (int64_t)sizeof(float), st)) != hipSuccess ||
            (e = zs::launch_fill_zero(reinterpret_cast<float*>(a.gcount),
@@ -132,9 +134,8 @@ zero_status_t bind(zero_grads_t h, void* const* src, void* const* dst, hipStream
   DeviceGuard dg(h->device);
   zs::GradsBindArgs a;
   a.chunks = const_cast<zs::GradsChunk*>(h->args.chunks);
-  char* ws = reinterpret_cast<char*>(h->args.sc);
-  a.offsets = reinterpret_cast<zs::GradsOffset*>(ws + h->plan.layout.offsets);
-  a.ranges = reinterpret_cast<zs::GradsRange*>(ws + h->plan.layout.ranges);
+  a.offsets = reinterpret_cast<zs::GradsOffset*>(reinterpret_cast<char*>(h->args.sc) + h->plan.layout.offsets);
+  a.ranges = h->args.ranges;
   for (int64_t i = 0; i < n; i += zs::kGradsBind) {
     const int m = (int)(n - i < zs::kGradsBind ? n - i : zs::kGradsBind);
     a.first = (int32_t)i;

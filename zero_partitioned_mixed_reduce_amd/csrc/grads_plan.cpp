@@ -156,7 +156,7 @@ zero_status_t build_grads_plan(const zero_grads_tensor_t* tensors, int64_t n, Gr
   p.tensors.assign(tensors, tensors + n);
   p.in_place.resize((size_t)n);
   memset(&p.info, 0, sizeof(p.info));
-  p.bytes_in = 0;
+  p.bytes_in = p.n_empty = 0;
   p.all16 = true;
   for (int64_t i = 0; i < n; ++i) {
     zero_grads_tensor_t& t = p.tensors[i];
@@ -182,6 +182,7 @@ zero_status_t build_grads_plan(const zero_grads_tensor_t* tensors, int64_t n, Gr
     if (t.rows > 1 && len > 0 && (t.dst_pitch < t.cols || t.dst_pitch > kMaxElems / t.rows))
       return bad(err, i, "dst_pitch must be at least cols, and the tensor's span at most 2^60 elements");
     if (len == 0) {
+      ++p.n_empty;
       t.rows = 1;
       t.cols = 0;
     }
