@@ -56,3 +56,29 @@ def test_exchanges_step_after_step(kind):
             for h, g in zip(hs, grads):
                 want = g[i].cpu().double() * c_of(norm, limit)
                 assert ((h._out[i].cpu().double() - want).abs() <= 4 * H * want.abs() + 2.0 ** -149).all(), (step, i)
+
+
+def test_bind_refuses_negated_views():
+    """Sources and destinations whose memory holds the opposite sign, as the constructor refuses them."""
+    z = torch.complex(torch.ones(300), torch.full((300,), 2.0)).cuda()
+    x, y = torch.ones(4, device="cuda"), torch.ones(4, device="cuda")
+    for plain, neg in ((z.imag, z.conj().imag), (y, torch._neg_view(y))):
+        into = torch.zeros(4 + plain.numel(), device="cuda")
+        for out, bad in ((None, ([x, neg], None)), (into, ([x, neg], into)), ([into[:4], into[4:]], ([x, neg], [into[:4], into[4:]]))):
+            with pytest.raises(ValueError, match="negated"):
+                ZeroGrads([x, neg], out=out)
+            h = ZeroGrads([x, plain], out=out)
+            with pytest.raises(ValueError, match="negated"):
+                h.zero_grads_bind(*bad)
+            h.zero_grads_norm()                       # the plan's own addresses stand
+            assert float(h.acc) == 4.0 + float((plain.cpu().double() ** 2).sum())
+    flat = torch.zeros(4, device="cuda")
+    h = ZeroGrads([x], out=flat)
+    with pytest.raises(ValueError, match="negated"):
+        h.zero_grads_bind([x], torch._neg_view(flat))
+    h = ZeroGrads([x], out=[flat])
+    with pytest.raises(ValueError, match="negated"):
+        h.zero_grads_bind([x], [torch._neg_view(flat)])
+    for bad in ([None], [3], [x.to_sparse()], [x.cpu()]):
+        with pytest.raises(ValueError):
+            h.zero_grads_bind(bad, [flat])
