@@ -40,6 +40,14 @@
  *   - All calls but init, query and destroy only enqueue kernels, and nothing
  *     of a result is kept on the host, so they can be captured into a HIP graph
  *     and replayed.  The arguments (addresses, inv, max_norm) are fixed in it.
+ *     A captured call has run when its graph is replayed and not before, and
+ *     every replay counts as its calls: a clip goes by the norm that ran last,
+ *     its kind and inverse scale, wherever the two were captured or not.
+ *   - The host does not see replays.  Once a zero_grads_norm of the handle has
+ *     been captured, or where a replay comes between a norm and its clip, the
+ *     device judges: a clip that finds no norm of these values there (or, for
+ *     ZERO_CLIP_EACH, none with per_tensor) writes nothing, and the
+ *     zero_grads_query behind it returns ZERO_ESTATE.
  *   - Calls on one handle must not overlap, replays of graphs captured from it
  *     included: they share its workspace.  Different handles are independent.
  */
@@ -148,7 +156,7 @@ zero_status_t zero_grads_scale(zero_grads_t h, float factor, void* stream);
 /* What the last zero_grads_clip (or zero_grads_clip_norm) used: the global norm,
  * whether the flag was set, and the global coefficient (1 for ZERO_CLIP_EACH).
  * Any output pointer may be NULL.  Synchronises the stream.  ESTATE before the
- * first clip. */
+ * first clip has run, and when the last one found no norm. */
 zero_status_t zero_grads_query(zero_grads_t h, double* norm, int32_t* found_inf, float* coef, void* stream);
 
 /* Frees the host handle (never caller memory). */

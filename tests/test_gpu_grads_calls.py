@@ -82,3 +82,123 @@ def test_bind_refuses_negated_views():
     for bad in ([None], [3], [x.to_sparse()], [x.cpu()]):
         with pytest.raises(ValueError):
             h.zero_grads_bind(bad, [flat])
+
+
+def refused_by_the_device(h, out):
+    """A clip that finds no norm of the values on the device: nothing written, and the query says so."""
+    assert all((o == 7).all() for o in out)
+    with pytest.raises(ZeroError) as e:
+        h.query()
+    assert e.value.status == _abi.ZERO_ESTATE
+
+
+def captured(*calls):
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for f in calls:
+            f()
+    return g
+
+
+def two_lists(seed=1):
+    grads = [rand(seed + i, n, torch.bfloat16) for i, n in enumerate((5000, 70_000, 3, 900))]
+    out = [torch.full((g.numel(),), 7.0, device="cuda") for g in grads]
+    return grads, out, ZeroGrads(grads, out=out)
+
+
+def renew(grads, out, seed):
+    for i, (g, o) in enumerate(zip(grads, out)):
+        g.copy_(rand(seed + i, g.numel(), torch.bfloat16))
+        o.fill_(7.0)
+
+
+def check_clipped(h, grads, out, kind, inv, max_norm, scope=GLOBAL):
+    """The list as this norm, inverse scale and limit clip it, by the formula and, given the coefficient, to the bit."""
+    sizes, whole = check_norms(h, grads, kind, inv, scope == EACH)
+    q = h.query()
+    assert abs(q["norm"] - whole) <= 1.25 * H * whole and not q["found_inf"]
+    for i, (g, o) in enumerate(zip(grads, out)):
+        acc = float(h.tensor_acc[i])
+        coef = (float(np.float32(c_of(acc if kind == MAX else math.sqrt(acc), max_norm))) if scope == EACH else
+                float(np.float32(c_of(q["norm"], max_norm))))
+        assert (bits(o) == bits(emulate(g, inv, coef, torch.float32))).all()
+    return q
+
+
+def test_captured_norm_and_clip_beside_it():
+    """The norm in a graph and the clip at once or in another graph, step after step, as around an exchange that is not
+    captured: the clip goes by the norm that ran last, its kind and inverse scale."""
+    for kind, inv, scope in ((L2, 0.5, GLOBAL), (MAX, 0.25, EACH)):
+        grads, out, h = two_lists()
+        norm = captured(lambda: h.zero_grads_norm(kind, inv, per_tensor=True))
+        h.zero_grads_clip(1e-3, scope)                # the graph has not run: there is no norm
+        refused_by_the_device(h, out)
+        clip = captured(lambda: h.zero_grads_clip(1e-3, scope))
+        with pytest.raises(ZeroError):                # nor has this one
+            h.query()
+        for step in range(4):
+            renew(grads, out, 100 * step)
+            norm.replay()
+            if step % 2:
+                clip.replay()
+            else:
+                h.zero_grads_clip(1e-3, scope)
+            check_clipped(h, grads, out, kind, inv, 1e-3, scope)
+            for o in out:
+                o.fill_(7.0)
+            if step % 2:
+                h.zero_grads_clip(1e-3, scope)        # a second clip of the same norm
+            else:
+                clip.replay()
+            refused_by_the_device(h, out)
+        # an eager norm of another kind and scale, then the captured clip, and the other way round
+        for first, k, i in ((lambda: h.zero_grads_norm(3 - kind, 2.0, per_tensor=True), 3 - kind, 2.0), (norm.replay, kind, inv)):
+            for then in (clip.replay, lambda: h.zero_grads_clip(1e-3, scope)):
+                renew(grads, out, 7)
+                h.zero_grads_norm(kind, inv, per_tensor=True)
+                norm.replay()
+                first()
+                then()
+                check_clipped(h, grads, out, k, i, 1e-3, scope)
+
+
+def test_replays_between_a_norm_and_its_clip():
+    """Replayed calls count as calls: one that takes another norm replaces the first, one that writes ends it."""
+    grads, out, h = two_lists()
+    other = captured(lambda: h.zero_grads_norm(MAX, 0.25))
+    write = captured(lambda: h.zero_grads_scale(3.0))
+    renew(grads, out, 5)
+    h.zero_grads_norm(L2, 0.5, per_tensor=True)
+    other.replay()
+    h.zero_grads_clip(1e-3)
+    check_clipped(h, grads, out, MAX, 0.25, 1e-3)
+    renew(grads, out, 6)
+    h.zero_grads_norm(L2, 0.5, per_tensor=True)
+    other.replay()
+    h.zero_grads_clip(1e-3, EACH)                     # the norm that ran last has no per-tensor norms
+    refused_by_the_device(h, out)
+    h.zero_grads_norm(L2, 0.5, per_tensor=True)
+    write.replay()
+    for o in out:
+        o.fill_(7.0)
+    h.zero_grads_clip(1e-3)
+    refused_by_the_device(h, out)
+    h.zero_grads_clip_norm(1e-3, L2, 0.5)             # both in one call are never apart
+    check_clipped(h, grads, out, L2, 0.5, 1e-3)
+    both = captured(lambda: h.zero_grads_norm(L2, 2.0, per_tensor=True), lambda: h.zero_grads_clip(1e-3, EACH))
+    for step in range(3):
+        renew(grads, out, 50 + step)
+        both.replay()
+        check_clipped(h, grads, out, L2, 2.0, 1e-3, EACH)
+        h.zero_grads_norm(MAX)
+    # without any norm in a graph the host knows, and says so at once
+    grads, out, h = two_lists()
+    captured(lambda: h.zero_grads_scale(1.0))
+    with pytest.raises(ZeroError) as e:
+        h.zero_grads_clip(1.0)
+    assert e.value.status == _abi.ZERO_ESTATE
+    h.zero_grads_norm()
+    captured(lambda: h.zero_grads_scale(1.0))         # has not run: the norm stands
+    h.zero_grads_clip(1e-3)
+    check_clipped(h, grads, out, L2, 1.0, 1e-3)

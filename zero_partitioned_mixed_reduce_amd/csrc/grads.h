@@ -72,7 +72,12 @@ struct GradsRange {
   int32_t first, count;
 };
 
-// Device-resident results (first 256 bytes of the workspace).
+// What GradsScalars::have says of the results.
+constexpr int32_t kGradsNorm = 1;       // acc and flag are those of the list's present values
+constexpr int32_t kGradsPerTensor = 2;  // ... and tensor_acc with them
+
+// Device-resident results (first 256 bytes of the workspace), and which of them a clip may use:
+// only the device sees the replays of captured calls.
 struct alignas(256) GradsScalars {
   double acc;        // sum of squares, or the largest magnitude
   int32_t flag;      // acc is not finite
@@ -81,6 +86,11 @@ struct alignas(256) GradsScalars {
   float coef;        // global coefficient of the last clip
   double clip_norm;  // global norm of the last clip
   int32_t clip_flag;
+  int32_t have;      // kGradsNorm, kGradsPerTensor; 0 once the values have been written or bound anew
+  int32_t kind;      // of the norm that ran last: zero_norm_t and inverse loss scale
+  float inv;
+  int32_t refused;   // the last clip found no norm that it could use, and wrote nothing
+  int32_t clipped;   // a clip has left its norm here
 };
 static_assert(sizeof(GradsScalars) == 256, "scalar block");
 
@@ -128,6 +138,7 @@ struct GradsBindArgs {
   GradsChunk* chunks;
   const GradsOffset* offsets;
   const GradsRange* ranges;
+  GradsScalars* sc;
   int32_t first;  // index of the first tensor
   uint64_t src[kGradsBind], dst[kGradsBind];
 };

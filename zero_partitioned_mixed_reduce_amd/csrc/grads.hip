@@ -238,7 +238,7 @@ __device__ __forceinline__ void walk_item(Op& op, const GradsChunk& k, int t) {
 // elements more than its memory traffic (1.56e9 bf16 elements: 1308 us instead of 1001).
 struct ClipArgs {
   int32_t now;
-  int32_t norm, scope;
+  int32_t scope;
   float max_norm;
   int32_t other_flag;
   double other_acc;
@@ -359,22 +359,27 @@ __device__ __forceinline__ float coefficient(double norm, bool bad, float max_no
 }
 
 // Records the global norm to clip by and its coefficient.
-__device__ __forceinline__ void clip_by(GradsScalars* sc, double acc, bool bad, const ClipArgs& c) {
-  const double norm = c.norm == ZERO_NORM_L2 ? sqrt(acc) : acc;
+__device__ __forceinline__ void clip_by(GradsScalars* sc, double norm, bool bad, const ClipArgs& c) {
   sc->norm = (float)norm;
   sc->coef = c.scope == ZERO_CLIP_GLOBAL ? coefficient(norm, bad, c.max_norm) : 1.0f;
   sc->clip_norm = norm;
   sc->clip_flag = bad;
+  sc->refused = 0;
+  sc->clipped = 1;
 }
 
 // The list's results, once per pass.
 template <int KIND>
-__device__ __forceinline__ void finish_list(typename Acc<KIND>::V v, GradsScalars* sc, const ClipArgs& clip) {
-  const double acc = Acc<KIND>::acc(v);
+__device__ __forceinline__ void finish_list(typename Acc<KIND>::V v, GradsScalars* sc, float inv, int per_tensor,
+                                            const ClipArgs& clip) {
+  const double acc = Acc<KIND>::acc(v), norm = norm_of<KIND>(acc);
   sc->acc = acc;
   sc->flag = !__builtin_isfinite(acc);
-  sc->norm = (float)norm_of<KIND>(acc);
-  if (clip.now) clip_by(sc, acc, !__builtin_isfinite(acc), clip);
+  sc->norm = (float)norm;
+  sc->have = clip.now ? 0 : per_tensor ? kGradsNorm | kGradsPerTensor : kGradsNorm;
+  sc->kind = KIND;
+  sc->inv = inv;
+  if (clip.now) clip_by(sc, norm, !__builtin_isfinite(acc), clip);
 }
 // A tensor's results.  The coefficient is the one without the flag, which another tensor may
 // yet set; what reads it goes by the flag first.
@@ -463,7 +468,7 @@ struct ItemEnd {
 // re-armed by their last arrival.
 template <int KIND>
 __device__ void norm_block_end(typename Acc<KIND>::V item, int n_items, int first_item, const ItemEnd* ends,
-                               const GradsArgs& a, int per_tensor, const ClipArgs& clip) {
+                               const GradsArgs& a, float inv, int per_tensor, const ClipArgs& clip) {
   typedef Acc<KIND> A;
   const int lane = (int)threadIdx.x;
   typename A::V v = __shfl(item, 0, 64);
@@ -514,7 +519,7 @@ __device__ void norm_block_end(typename Acc<KIND>::V item, int n_items, int firs
   if (__shfl(before, 63, 64) + 1 != gsize) return;
   if (lane == 0) rearm(a.gcount + kGradsPitch / 4 * g);
   if (join_level<A>(nb, ngroups, a.part, g0, gsize, a.gpart, g, &a.sc->counter, &v) && lane == 0)
-    finish_list<KIND>(v, a.sc, clip);
+    finish_list<KIND>(v, a.sc, inv, per_tensor, clip);
 }
 
 // A block takes a.run consecutive block items, so that what ends a block -- its sum, a store, an
@@ -575,7 +580,7 @@ __global__ void __launch_bounds__(kGradsBlock, 7) grads_norm_kernel(GradsArgs a,
     if (wave != 0) return;
     if (lane < n_items) item = sums[lane][0];
   }
-  norm_block_end<KIND>(item, n_items, first, ends, a, per_tensor, clip);
+  norm_block_end<KIND>(item, n_items, first, ends, a, inv, per_tensor, clip);
 }
 
 // What no item finishes: the norms of tensors without elements, 0 in every pass (an exchange may
@@ -583,27 +588,36 @@ __global__ void __launch_bounds__(kGradsBlock, 7) grads_norm_kernel(GradsArgs a,
 // for lists that have such tensors: looked for in the norm kernel they cost every list, 483 us
 // for the 477 of 1.56e9 bf16 elements.
 template <int KIND>
-__global__ void __launch_bounds__(kGradsBlock) grads_empty_kernel(GradsArgs a, int per_tensor, int list, ClipArgs clip) {
+__global__ void __launch_bounds__(kGradsBlock) grads_empty_kernel(GradsArgs a, float inv, int per_tensor,
+                                                                  int list, ClipArgs clip) {
   const int i = (int)blockIdx.x * kGradsBlock + (int)threadIdx.x;
   if (per_tensor && i < a.n_tensors && a.ranges[i].count == 0) {
     a.tensor_acc[i] = 0.0;
     a.norms[i] = 0.0f;
   }
-  if (list && i == 0) finish_list<KIND>(Acc<KIND>::none(), a.sc, clip);
+  if (list && i == 0) finish_list<KIND>(Acc<KIND>::none(), a.sc, inv, per_tensor, clip);
 }
 
 // The coefficients of a clip from the results on the device, as the norm call and an exchange
-// have left them, and other ranks'.
+// have left them, and other ranks'.  Which norm that was, and whether the values are still the
+// ones it was taken of, is read here and not passed: a replay of captured calls may have come
+// between.  The first thread decides for all; the other coefficients are not used if it refuses.
 __global__ void __launch_bounds__(kGradsBlock) grads_coefs_kernel(GradsArgs a, ClipArgs c) {
-  double acc = a.sc->acc;
-  if (c.norm == ZERO_NORM_L2) acc += c.other_acc;
-  else acc = c.other_acc > acc || __builtin_isnan(c.other_acc) ? c.other_acc : acc;
-  const bool bad = (a.sc->flag | c.other_flag) != 0 || !__builtin_isfinite(acc);
+  const bool l2 = a.sc->kind == ZERO_NORM_L2;
   const int i = (int)blockIdx.x * kGradsBlock + (int)threadIdx.x;
-  if (i == 0) clip_by(a.sc, acc, bad, c);
+  if (i == 0) {
+    const int32_t need = c.scope == ZERO_CLIP_EACH ? kGradsNorm | kGradsPerTensor : kGradsNorm;
+    double acc = a.sc->acc;
+    if (l2) acc += c.other_acc;
+    else acc = c.other_acc > acc || __builtin_isnan(c.other_acc) ? c.other_acc : acc;
+    const bool bad = (a.sc->flag | c.other_flag) != 0 || !__builtin_isfinite(acc);
+    if ((a.sc->have & need) == need) clip_by(a.sc, l2 ? sqrt(acc) : acc, bad, c);
+    else a.sc->refused = 1;
+    a.sc->have = 0;
+  }
   if (c.scope == ZERO_CLIP_EACH && i < a.n_tensors) {
     const double t = a.tensor_acc[i];
-    a.coefs[i] = coefficient(c.norm == ZERO_NORM_L2 ? sqrt(t) : t, false, c.max_norm);
+    a.coefs[i] = coefficient(l2 ? sqrt(t) : t, false, c.max_norm);
   }
 }
 
@@ -667,9 +681,13 @@ __device__ __forceinline__ void scale_any(const GradsChunk& k, float inv, float 
   else scale_to<ZERO_F16, W, NT>(k, inv, coef, t);
 }
 
+// By what else than `inv` and the coefficients a list is scaled: nothing; nothing, and the norm
+// that stands is ended; the inverse scale of the norm on the device, unless a clip was refused.
+enum ScaleBy { kScaleByArgs = 0, kScaleEndsNorm = 1, kScaleByNorm = 2 };
+
 // One of `parts` parts of a block item per block, or four wave items; by inv and, for a clip,
 // the coefficients found for it.
-__global__ void __launch_bounds__(kGradsBlock) grads_scale_kernel(GradsArgs a, float inv, int scope, int parts) {
+__global__ void __launch_bounds__(kGradsBlock) grads_scale_kernel(GradsArgs a, float inv, int scope, int by, int parts) {
   const int b = (int)blockIdx.x;
   const int whole = a.n_block_items * parts;
   const bool by_wave = b >= whole;
@@ -681,6 +699,12 @@ __global__ void __launch_bounds__(kGradsBlock) grads_scale_kernel(GradsArgs a, f
   const float coef = scope == ZERO_CLIP_GLOBAL                       ? a.sc->coef
                      : scope == ZERO_CLIP_EACH && !a.sc->clip_flag ? a.coefs[k.tensor]
                                                                    : 1.0f;
+  if (by == kScaleByNorm) {
+    inv = a.sc->inv;
+    if (a.sc->refused) return;
+  } else if (by == kScaleEndsNorm && b == 0 && threadIdx.x == 0) {
+    a.sc->have = 0;  // behind the loads above, which would not be scalar ones after a store
+  }
   if (inv == 1.0f && coef == 1.0f && k.src == k.dst) return;  // in place and nothing to change
   if (by_wave) {
     scale_any<64, false>(k, inv, coef, (int)threadIdx.x & 63);
@@ -711,6 +735,7 @@ __global__ void __launch_bounds__(kGradsBlock) grads_scale_kernel(GradsArgs a, f
 __global__ void __launch_bounds__(kGradsBlock) grads_bind_kernel(GradsBindArgs a) {
   const int b = (int)blockIdx.x;
   const GradsRange r = a.ranges[a.first + b];
+  if (b == 0 && threadIdx.x == 0) a.sc->have = 0;
   for (int c = (int)threadIdx.x; c < r.count; c += kGradsBlock) {
     GradsChunk* k = a.chunks + r.first + c;
     const GradsOffset o = a.offsets[r.first + c];
@@ -729,7 +754,8 @@ static hipError_t launch_norm(const GradsArgs& a, float inv, bool per_tensor, co
   const unsigned g = (unsigned)((a.n_block_items + a.run - 1) / a.run + (a.n_blocks - a.n_block_items));
   if (g == 0 || (per_tensor && a.n_empty > 0)) {
     const unsigned ge = per_tensor ? (unsigned)((a.n_tensors - 1) / kGradsBlock + 1) : 1u;
-    hipLaunchKernelGGL(grads_empty_kernel<KIND>, dim3(ge), dim3(kGradsBlock), 0, st, a, (int)per_tensor, (int)(g == 0), c);
+    hipLaunchKernelGGL(grads_empty_kernel<KIND>, dim3(ge), dim3(kGradsBlock), 0, st, a, inv, (int)per_tensor,
+                       (int)(g == 0), c);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || g == 0) return e;
   }
@@ -747,14 +773,14 @@ static hipError_t launch_norm_of(const GradsArgs& a, int norm, float inv, bool p
 }
 
 // scope 0: by inv alone.
-static hipError_t launch_scaling(const GradsArgs& a, float inv, int scope, hipStream_t st) {
+static hipError_t launch_scaling(const GradsArgs& a, float inv, int scope, ScaleBy by, hipStream_t st) {
   if (a.n_blocks == 0) return hipSuccess;
   // A block for 8 KiB of the wider side: short-lived blocks of one or two groups per lane keep
   // reads and writes in step (bf16 to bf16, 1.56e9 elements: 1156 us with whole items, 1012
   // with halves, 1030 with quarters; fp32 to bf16, 4.1e8: 445, 415 and 361; eighths 1350 and 450).
   const int parts = a.all16 ? 2 : 4;
   const unsigned g = (unsigned)(a.n_blocks + (int64_t)a.n_block_items * (parts - 1));
-  hipLaunchKernelGGL(grads_scale_kernel, dim3(g), dim3(kGradsBlock), 0, st, a, inv, scope, parts);
+  hipLaunchKernelGGL(grads_scale_kernel, dim3(g), dim3(kGradsBlock), 0, st, a, inv, scope, (int)by, parts);
   return hipGetLastError();
 }
 
@@ -762,23 +788,24 @@ hipError_t launch_grads_norm(const GradsArgs& a, int norm, float inv, bool per_t
   return launch_norm_of(a, norm, inv, per_tensor, ClipArgs{}, st);
 }
 
-hipError_t launch_grads_clip(const GradsArgs& a, int norm, int scope, float inv, int other_flag, double other_acc,
-                             float max_norm, hipStream_t st) {
-  const ClipArgs c{1, norm, scope, max_norm, other_flag, other_acc};
+hipError_t launch_grads_clip(const GradsArgs& a, int scope, int other_flag, double other_acc, float max_norm,
+                             hipStream_t st) {
+  const ClipArgs c{1, scope, max_norm, other_flag, other_acc};
   const unsigned g = scope == ZERO_CLIP_EACH ? (unsigned)((a.n_tensors - 1) / kGradsBlock + 1) : 1u;
   hipLaunchKernelGGL(grads_coefs_kernel, dim3(g), dim3(kGradsBlock), 0, st, a, c);
-  return launch_scaling(a, inv, scope, st);
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess ? e : launch_scaling(a, 1.0f, scope, kScaleByNorm, st);
 }
 
 hipError_t launch_grads_clip_norm(const GradsArgs& a, int norm, float inv, bool per_tensor, int scope, float max_norm,
                                   hipStream_t st) {
-  const ClipArgs c{1, norm, scope, max_norm, 0, 0.0};
+  const ClipArgs c{1, scope, max_norm, 0, 0.0};
   hipError_t e = launch_norm_of(a, norm, inv, per_tensor, c, st);
-  return e != hipSuccess ? e : launch_scaling(a, inv, scope, st);
+  return e != hipSuccess ? e : launch_scaling(a, inv, scope, kScaleByArgs, st);
 }
 
-hipError_t launch_grads_scale(const GradsArgs& a, float factor, hipStream_t st) {
-  return launch_scaling(a, factor, 0, st);
+hipError_t launch_grads_scale(const GradsArgs& a, float factor, bool ends_norm, hipStream_t st) {
+  return launch_scaling(a, factor, 0, ends_norm ? kScaleEndsNorm : kScaleByArgs, st);
 }
 
 hipError_t launch_grads_bind(const GradsBindArgs& a, int n, hipStream_t st) {

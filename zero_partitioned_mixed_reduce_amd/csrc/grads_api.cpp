@@ -16,11 +16,11 @@ struct zero_grads {
   zs::GradsPlan plan;
   zs::GradsArgs args;
   int device;
-  bool has_norm;    // acc and flag on the device are those of the list's present values
-  bool per_tensor;  // ... and tensor_acc with them
-  bool clipped;     // a clip has reported its norm
-  int32_t norm;
-  float inv;
+  // Norms that a clip may find on the device (kGradsNorm, kGradsPerTensor).  What is captured runs
+  // when its graph is replayed, unseen here: the device knows what has run (GradsScalars::have),
+  // and the host refuses only what no replay can have made right.
+  int32_t have;        // of the calls that were not captured
+  int32_t graph_have;  // of all captured norms
 };
 
 namespace {
@@ -31,6 +31,16 @@ using zs::set_error;
 zero_status_t fail(zero_status_t s, const std::string& msg) { return set_error(s, msg); }
 zero_status_t hip_fail(const char* what, hipError_t e) {
   return set_error(ZERO_EHIP, std::string(what) + ": " + hipGetErrorString(e));
+}
+
+// A stream that cannot tell is not captured: its calls fail by themselves.
+bool capturing(hipStream_t st) {
+  hipStreamCaptureStatus s = hipStreamCaptureStatusNone;
+  if (hipStreamIsCapturing(st, &s) != hipSuccess) {
+    (void)hipGetLastError();
+    return false;
+  }
+  return s != hipStreamCaptureStatusNone;
 }
 
 zero_status_t init(const zero_grads_tensor_t* tensors, int64_t n, void* workspace, int64_t workspace_capacity,
@@ -105,9 +115,7 @@ zero_status_t init(const zero_grads_tensor_t* tensors, int64_t n, void* workspac
   h->plan = std::move(p);
   h->args = a;
   h->device = dev;
-  h->has_norm = h->per_tensor = h->clipped = false;
-  h->norm = ZERO_NORM_L2;
-  h->inv = 1.0f;
+  h->have = h->graph_have = 0;
   *out = h;
   return ZERO_OK;
 }
@@ -136,6 +144,7 @@ zero_status_t bind(zero_grads_t h, void* const* src, void* const* dst, hipStream
   a.chunks = const_cast<zs::GradsChunk*>(h->args.chunks);
   a.offsets = reinterpret_cast<zs::GradsOffset*>(reinterpret_cast<char*>(h->args.sc) + h->plan.layout.offsets);
   a.ranges = h->args.ranges;
+  a.sc = h->args.sc;
   for (int64_t i = 0; i < n; i += zs::kGradsBind) {
     const int m = (int)(n - i < zs::kGradsBind ? n - i : zs::kGradsBind);
     a.first = (int32_t)i;
@@ -148,8 +157,13 @@ zero_status_t bind(zero_grads_t h, void* const* src, void* const* dst, hipStream
   }
   h->plan.tensors = std::move(t);
   h->plan.overlap = overlap;
-  h->has_norm = false;
+  h->have = 0;
   return ZERO_OK;
+}
+
+// A call that writes the list's values has been enqueued: the norm is not theirs any more.
+void written(zero_grads_t h, void* stream) {
+  if (!capturing(static_cast<hipStream_t>(stream))) h->have = 0;
 }
 
 // Calls that write refuse a list in which tensors without a destination overlap.
@@ -221,10 +235,9 @@ zero_status_t zero_grads_norm(zero_grads_t h, int32_t norm, float inv_loss_scale
   DeviceGuard dg(h->device);
   hipError_t e = zs::launch_grads_norm(h->args, norm, inv_loss_scale, per_tensor != 0, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail("norm kernel", e);
-  h->has_norm = true;
-  h->per_tensor = per_tensor != 0;
-  h->norm = norm;
-  h->inv = inv_loss_scale;
+  const int32_t have = per_tensor ? zs::kGradsNorm | zs::kGradsPerTensor : zs::kGradsNorm;
+  if (capturing(static_cast<hipStream_t>(stream))) h->graph_have |= have;
+  else h->have = have;
   return ZERO_OK;
 }
 
@@ -246,15 +259,15 @@ zero_status_t zero_grads_clip(zero_grads_t h, int32_t scope, int32_t other_ranks
   if (s != ZERO_OK) return s;
   if ((s = check_writable(h)) != ZERO_OK) return s;
   if (other_ranks_acc < 0.0) return fail(ZERO_EINVAL, "other_ranks_acc must not be negative");
-  if (!h->has_norm) return fail(ZERO_ESTATE, "zero_grads_clip must follow zero_grads_norm of the same values");
-  if (scope == ZERO_CLIP_EACH && !h->per_tensor)
+  const int32_t have = h->have | h->graph_have;
+  if (!have) return fail(ZERO_ESTATE, "zero_grads_clip must follow zero_grads_norm of the same values");
+  if (scope == ZERO_CLIP_EACH && !(have & zs::kGradsPerTensor))
     return fail(ZERO_ESTATE, "ZERO_CLIP_EACH needs a zero_grads_norm with per_tensor");
   DeviceGuard dg(h->device);
-  hipError_t e = zs::launch_grads_clip(h->args, h->norm, scope, h->inv, other_ranks_found_inf != 0, other_ranks_acc,
-                                       max_norm, static_cast<hipStream_t>(stream));
+  hipError_t e = zs::launch_grads_clip(h->args, scope, other_ranks_found_inf != 0, other_ranks_acc, max_norm,
+                                       static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail("clip kernel", e);
-  h->has_norm = false;
-  h->clipped = true;
+  written(h, stream);
   return ZERO_OK;
 }
 
@@ -268,8 +281,7 @@ zero_status_t zero_grads_clip_norm(zero_grads_t h, int32_t norm, float inv_loss_
   hipError_t e = zs::launch_grads_clip_norm(h->args, norm, inv_loss_scale, per_tensor != 0 || scope == ZERO_CLIP_EACH,
                                             scope, max_norm, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail("norm and clip kernels", e);
-  h->has_norm = false;
-  h->clipped = true;
+  written(h, stream);
   return ZERO_OK;
 }
 
@@ -279,21 +291,25 @@ zero_status_t zero_grads_scale(zero_grads_t h, float factor, void* stream) {
   zero_status_t s = check_writable(h);
   if (s != ZERO_OK) return s;
   DeviceGuard dg(h->device);
-  hipError_t e = zs::launch_grads_scale(h->args, factor, static_cast<hipStream_t>(stream));
+  // the device has a norm to end if the host knows of one, or cannot know
+  const bool ends_norm = h->have || h->graph_have || capturing(static_cast<hipStream_t>(stream));
+  hipError_t e = zs::launch_grads_scale(h->args, factor, ends_norm, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail("scale kernel", e);
-  h->has_norm = false;
+  written(h, stream);
   return ZERO_OK;
 }
 
 zero_status_t zero_grads_query(zero_grads_t h, double* norm, int32_t* found_inf, float* coef, void* stream) {
   if (!h) return fail(ZERO_EINVAL, "null handle");
-  if (!h->clipped) return fail(ZERO_ESTATE, "no zero_grads_clip yet");
   DeviceGuard dg(h->device);
   zs::GradsScalars sc;
   hipError_t e = hipStreamSynchronize(static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail("hipStreamSynchronize(query)", e);
   e = hipMemcpy(&sc, h->args.sc, sizeof(sc), hipMemcpyDeviceToHost);
   if (e != hipSuccess) return hip_fail("hipMemcpy(scalars)", e);
+  if (sc.refused)
+    return fail(ZERO_ESTATE, "the last zero_grads_clip found no norm of these values on the device, and wrote nothing");
+  if (!sc.clipped) return fail(ZERO_ESTATE, "no zero_grads_clip has run yet");
   if (norm) *norm = sc.clip_norm;
   if (found_inf) *found_inf = sc.clip_flag ? 1 : 0;
   if (coef) *coef = sc.coef;

@@ -57,10 +57,10 @@ hipError_t launch_adam_step(int dtype, int grad_source, bool cast, const Chunk* 
 // Kernel launchers of the gradient lists (grads.hip).
 namespace zs {
 hipError_t launch_grads_norm(const GradsArgs& a, int norm, float inv, bool per_tensor, hipStream_t st);
-hipError_t launch_grads_clip(const GradsArgs& a, int norm, int scope, float inv, int other_flag, double other_acc,
-                             float max_norm, hipStream_t st);
+hipError_t launch_grads_clip(const GradsArgs& a, int scope, int other_flag, double other_acc, float max_norm,
+                             hipStream_t st);
 hipError_t launch_grads_clip_norm(const GradsArgs& a, int norm, float inv, bool per_tensor, int scope, float max_norm,
                                   hipStream_t st);
-hipError_t launch_grads_scale(const GradsArgs& a, float factor, hipStream_t st);
+hipError_t launch_grads_scale(const GradsArgs& a, float factor, bool ends_norm, hipStream_t st);
 hipError_t launch_grads_bind(const GradsBindArgs& a, int n, hipStream_t st);
 }  // namespace zs

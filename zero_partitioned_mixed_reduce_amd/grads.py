@@ -223,7 +223,8 @@ class ZeroGrads:
         abi.zero_grads_scale(self.h, factor, self._stream())
 
     def query(self):
-        """What the last clip used: dict(norm, found_inf, coef).  Synchronises the current stream."""
+        """What the last clip used: dict(norm, found_inf, coef).  Synchronises the current stream.  ZERO_ESTATE if it
+        found no norm of these values (replays of captured calls included) and so wrote nothing."""
         return abi.zero_grads_query(self.h, self._stream())
 
     def close(self):
