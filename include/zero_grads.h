@@ -32,22 +32,29 @@
  * streams, caller-owned device memory), and:
  *   - A handle is a plan for one list: its sizes, types and pitches.  The
  *     addresses may change from step to step (zero_grads_bind).  Calls use the
- *     device that was current at zero_grads_init.
+ *     device that was current at zero_grads_init.  They stand in the workspace:
+ *     a call works on those of the last bind that has run before it.
  *   - One pass is zero_grads_norm -> [exchange with other ranks] ->
  *     zero_grads_clip, or both in one call, zero_grads_clip_norm; zero_grads_scale
  *     stands alone.  A zero_grads_clip without the norm of these values before
  *     it (none yet, or clipped, scaled or bound since) returns ZERO_ESTATE.
  *   - All calls but init, query and destroy only enqueue kernels, and nothing
  *     of a result is kept on the host, so they can be captured into a HIP graph
- *     and replayed.  The arguments (addresses, inv, max_norm) are fixed in it.
- *     A captured call has run when its graph is replayed and not before, and
- *     every replay counts as its calls: a clip goes by the norm that ran last,
- *     its kind and inverse scale, wherever the two were captured or not.
+ *     and replayed.  The scalar arguments (inv, max_norm) and a bind's addresses
+ *     are fixed in it.  A captured call has run when its graph is replayed and
+ *     not before, and every replay counts as its calls: a clip goes by the norm
+ *     that ran last, its kind and inverse scale, and every call by the addresses
+ *     bound last, wherever they were captured or not.  So a graph without a bind
+ *     uses whatever is bound when it is replayed, and a list bound in a graph
+ *     stays bound behind it: its memory has to last until another bind has run
+ *     and the graph is not replayed any more.
  *   - The host does not see replays.  Once a zero_grads_norm of the handle has
  *     been captured, or where a replay comes between a norm and its clip, the
  *     device judges: a clip that finds no norm of these values there (or, for
  *     ZERO_CLIP_EACH, none with per_tensor) writes nothing, and the
- *     zero_grads_query behind it returns ZERO_ESTATE.
+ *     zero_grads_query behind it returns ZERO_ESTATE.  A list that takes norms
+ *     only (see zero_grads_plan) is not bound once a call that writes has been
+ *     captured, and once one has been bound in a graph the handle does not write.
  *   - Calls on one handle must not overlap, replays of graphs captured from it
  *     included: they share its workspace.  Different handles are independent.
  */
@@ -112,8 +119,10 @@ zero_status_t zero_grads_info(zero_grads_t h, zero_grads_info_t* out);
 /* Gives the list's tensors new addresses, in list order (host arrays [n], read
  * during the call): src[i], and dst[i] where the list was planned with a
  * destination (dst may be NULL when no tensor was).  Sizes, types and pitches
- * stay.  Enqueues small kernels that write the work table.  EINVAL on what
- * zero_grads_plan would refuse; the handle then keeps its addresses. */
+ * stay; a tensor planned in place is bound in place, and one planned with a
+ * destination is not.  Enqueues small kernels that write the work table.  EINVAL
+ * on what zero_grads_plan would refuse; the handle then keeps its addresses.
+ * After EHIP another bind has to come before any other call. */
 zero_status_t zero_grads_bind(zero_grads_t h, void* const* src, void* const* dst, void* stream);
 
 /* The list's norm, its flag, and with per_tensor != 0 every tensor's norm, on

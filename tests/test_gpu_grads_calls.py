@@ -202,3 +202,81 @@ def test_replays_between_a_norm_and_its_clip():
     captured(lambda: h.zero_grads_scale(1.0))         # has not run: the norm stands
     h.zero_grads_clip(1e-3)
     check_clipped(h, grads, out, L2, 1.0, 1e-3)
+
+
+def test_bind_in_a_graph_binds_when_replayed():
+    """Eager calls work on the list bound last by what has run; the handle keeps every list that its table may name."""
+    import weakref
+
+    def make(v):
+        return [torch.full((n,), v, device="cuda") for n in (5000, 7)], [torch.zeros(n, device="cuda") for n in (5000, 7)]
+
+    def holds(out, v):
+        return all((o == v).all() for o in out)
+
+    def kept(refs):
+        return [r() is not None for r in refs]
+
+    (a, oa), (b, ob) = make(1.0), make(10.0)
+    h = ZeroGrads(a, out=oa)
+    ra, rb = [[weakref.ref(t) for t in x] for x in (a + oa, b + ob)]
+    g = captured(lambda: h.zero_grads_bind(b, ob), lambda: h.zero_grads_scale(2.0))
+    late = captured(lambda: h.zero_grads_scale(7.0))  # has no bind of its own
+    watch = [t.view(-1) for t in oa], [t.view(-1) for t in ob]
+    del a, b, oa, ob
+    assert all(kept(ra)) and all(kept(rb))
+    h.zero_grads_scale(3.0)                           # the graph has not run
+    assert holds(watch[0], 3.0) and holds(watch[1], 0.0)
+    g.replay()
+    assert holds(watch[0], 3.0) and holds(watch[1], 20.0)
+    h.zero_grads_scale(5.0)
+    assert holds(watch[0], 3.0) and holds(watch[1], 50.0)
+    c, oc = make(100.0)
+    h.zero_grads_bind(c, oc)
+    assert not any(kept(ra[:2])) and all(kept(rb))    # oa are held by their views here
+    for _ in range(3):
+        h.zero_grads_scale(2.0)
+        assert holds(oc, 200.0) and holds(watch[0], 3.0)
+        late.replay()                                 # works on what is bound now
+        assert holds(oc, 700.0)
+        g.replay()
+        assert holds(watch[1], 20.0) and holds(oc, 700.0)
+        late.replay()
+        assert holds(watch[1], 70.0) and holds(oc, 700.0)
+        h.zero_grads_norm(per_tensor=True)
+        assert float(h.acc) == 5007 * 100.0
+        h.zero_grads_bind(c, oc)
+    torch.cuda.synchronize()
+    h.close()
+    assert not any(kept(rb[:2]))
+
+
+def test_graphs_and_lists_that_overlap():
+    """A list with overlapping tensors takes norms only, and neither a replay nor a later bind brings it to a call that
+    writes."""
+    x, y = torch.ones(3000, device="cuda"), torch.ones(3000, device="cuda")
+
+    def invalid(f, *a):
+        with pytest.raises(ZeroError) as e:
+            f(*a)
+        assert e.value.status == _abi.ZERO_EINVAL
+
+    h = ZeroGrads([x, y])
+    g = captured(lambda: h.zero_grads_scale(2.0))
+    invalid(h.zero_grads_bind, [x, x])                # the graph would write x twice
+    captured(h.zero_grads_norm, lambda: invalid(h.zero_grads_bind, [y, y]))
+    g.replay()
+    assert (x == 2).all() and (y == 2).all()
+    h = ZeroGrads([x, y])
+    g = captured(lambda: h.zero_grads_bind([x, x]), lambda: h.zero_grads_norm())
+    h.zero_grads_norm()
+    invalid(h.zero_grads_clip, 1.0)                   # a replay may have come before
+    invalid(h.zero_grads_scale, 3.0)
+    h.zero_grads_bind([x, y])
+    invalid(h.zero_grads_scale, 3.0)
+    g.replay()
+    assert float(h.acc) == 2 * 4.0 * 3000 and (x == 2).all() and (y == 2).all()
+    h = ZeroGrads([x, x])                             # bound apart at once, it writes
+    h.zero_grads_bind([x, y])
+    h.zero_grads_scale(0.5)
+    assert (x == 1).all() and (y == 1).all()

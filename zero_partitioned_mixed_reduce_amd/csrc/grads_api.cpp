@@ -21,6 +21,9 @@ struct zero_grads {
   // and the host refuses only what no replay can have made right.
   int32_t have;        // of the calls that were not captured
   int32_t graph_have;  // of all captured norms
+  // Any captured call may meet any list that is bound later, and any later call a list bound in a graph.
+  bool graph_writes;      // a call that writes has been captured
+  int64_t graph_overlap;  // of lists bound in captures: as GradsPlan::overlap
 };
 
 namespace {
@@ -116,6 +119,8 @@ zero_status_t init(const zero_grads_tensor_t* tensors, int64_t n, void* workspac
   h->args = a;
   h->device = dev;
   h->have = h->graph_have = 0;
+  h->graph_writes = false;
+  h->graph_overlap = -1;
   *out = h;
   return ZERO_OK;
 }
@@ -139,7 +144,12 @@ zero_status_t bind(zero_grads_t h, void* const* src, void* const* dst, hipStream
   int64_t overlap;
   zero_status_t s = zs::check_grads_addresses(t, h->plan.in_place, &overlap, &err);
   if (s != ZERO_OK) return fail(s, err);
+  if (overlap >= 0 && h->graph_writes)
+    return fail(ZERO_EINVAL, "tensor " + std::to_string(overlap) +
+                                 ": shares elements with another tensor of the list, and a captured call writes in place");
   DeviceGuard dg(h->device);
+  const bool graph = capturing(st);
+  if (!graph) h->have = 0;
   zs::GradsBindArgs a;
   a.chunks = const_cast<zs::GradsChunk*>(h->args.chunks);
   a.offsets = reinterpret_cast<zs::GradsOffset*>(reinterpret_cast<char*>(h->args.sc) + h->plan.layout.offsets);
@@ -155,21 +165,24 @@ zero_status_t bind(zero_grads_t h, void* const* src, void* const* dst, hipStream
     hipError_t e = zs::launch_grads_bind(a, m, st);
     if (e != hipSuccess) return hip_fail("bind kernel", e);
   }
-  h->plan.tensors = std::move(t);
-  h->plan.overlap = overlap;
-  h->have = 0;
+  if (!graph)
+    h->plan.overlap = overlap;
+  else if (overlap >= 0)
+    h->graph_overlap = overlap;
   return ZERO_OK;
 }
 
 // A call that writes the list's values has been enqueued: the norm is not theirs any more.
 void written(zero_grads_t h, void* stream) {
-  if (!capturing(static_cast<hipStream_t>(stream))) h->have = 0;
+  if (capturing(static_cast<hipStream_t>(stream))) h->graph_writes = true;
+  else h->have = 0;
 }
 
 // Calls that write refuse a list in which tensors without a destination overlap.
 zero_status_t check_writable(const zero_grads* h) {
-  if (h->plan.overlap < 0) return ZERO_OK;
-  return fail(ZERO_EINVAL, "tensor " + std::to_string(h->plan.overlap) +
+  const int64_t overlap = h->plan.overlap >= 0 ? h->plan.overlap : h->graph_overlap;
+  if (overlap < 0) return ZERO_OK;
+  return fail(ZERO_EINVAL, "tensor " + std::to_string(overlap) +
                                ": shares elements with another tensor of the list, and would be written in place");
 }
 

@@ -118,9 +118,9 @@ class ZeroGrads:
     Results in place are written behind autograd's back, as into detached tensors.
 
     Calls use the current stream of the tensors' device, and the handle keeps the tensors alive until it is bound
-    to others or closed; a captured graph needs the handle, whose workspace it uses.  As with any torch call,
-    tensors used on another stream than the one they were allocated on must be kept until that stream is done
-    with them."""
+    to others or closed, and those bound in a captured graph until it is closed; a captured graph needs the handle,
+    whose workspace it uses, and binds its list whenever it is replayed.  As with any torch call, tensors used on
+    another stream than the one they were allocated on must be kept until that stream is done with them."""
 
     def __init__(self, tensors, out=None):
         self._tensors = list(tensors)
@@ -131,6 +131,7 @@ class ZeroGrads:
         self._in_place = out is None
         dsts = self._check(self._tensors, out)
         self._out = out
+        self._in_graphs = []                    # lists bound in captures: (tensors, out)
         self.device = self._tensors[0].device   # with its index
         desc = (abi.zero_grads_tensor_t * len(self._tensors))(
             *[describe(i, s, d) for i, (s, d) in enumerate(zip(self._tensors, dsts))])
@@ -189,9 +190,16 @@ class ZeroGrads:
     def _stream(self):
         return torch._C._cuda_getCurrentRawStream(self.device.index)
 
+    def _capturing(self):
+        if torch.cuda.current_device() == self.device.index:
+            return torch.cuda.is_current_stream_capturing()
+        with torch.cuda.device(self.device):
+            return torch.cuda.is_current_stream_capturing()
+
     # calls of the C ABI, under its names
     def zero_grads_bind(self, tensors, out=None):
-        """The list's tensors at new addresses: the same dtypes, shapes and strides."""
+        """The list's tensors at new addresses: the same dtypes, shapes and strides.  In a capture: whenever the graph is
+        replayed, for the calls behind it."""
         tensors = list(tensors)
         if (out is None) != self._in_place:
             raise ValueError("the plan is in place: bind without out" if self._in_place
@@ -206,7 +214,10 @@ class ZeroGrads:
             out = list(out)
             dst = self._out_layout.addresses(out, "out tensors")
         abi.zero_grads_bind(self.h, src, dst, self._stream())
-        self._tensors, self._out = tensors, out
+        if self._capturing():                   # bound when the graph is replayed, and not now
+            self._in_graphs.append((tensors, out))
+        else:
+            self._tensors, self._out = tensors, out
 
     def zero_grads_norm(self, norm=abi.ZERO_NORM_L2, inv_loss_scale=1.0, per_tensor=False):
         abi.zero_grads_norm(self.h, norm, inv_loss_scale, per_tensor, self._stream())
@@ -231,6 +242,7 @@ class ZeroGrads:
         if self.h:
             abi.zero_grads_destroy(self.h)
             self.h = None
+        self._tensors, self._out, self._in_graphs = [], None, []
 
     def __del__(self):
         try:
