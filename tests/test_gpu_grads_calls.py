@@ -280,3 +280,25 @@ def test_graphs_and_lists_that_overlap():
     h.zero_grads_bind([x, y])
     h.zero_grads_scale(0.5)
     assert (x == 1).all() and (y == 1).all()
+
+
+def test_workspace_of_a_handle_closed_while_another_stream_works():
+    """The workspace's memory is not given to others before every stream that the handle used is done with it."""
+    grads = [rand(i, 5000 + i, torch.float32) for i in range(40)]
+    side = torch.cuda.Stream()
+    h = ZeroGrads(grads, out=[torch.empty_like(g) for g in grads])
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)                 # some milliseconds of work in front of the handle's
+        h.zero_grads_clip_norm(1e-3, per_tensor=True)
+    keep, at, size = h._out, h.workspace.data_ptr(), h.workspace.numel()
+    h.close()
+    del h
+    others = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert not side.query() and all(t.data_ptr() != at for t in others)
+    side.synchronize()
+    norm = math.sqrt(math.fsum(float((g.double() ** 2).sum()) for g in grads))
+    coef = c_of(norm, 1e-3)
+    for o, g in zip(keep, grads):
+        want = g.double() * coef
+        assert ((o.double() - want).abs() <= 4 * H * want.abs() + 2.0 ** -149).all()

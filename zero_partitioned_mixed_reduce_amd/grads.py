@@ -119,8 +119,9 @@ class ZeroGrads:
 
     Calls use the current stream of the tensors' device, and the handle keeps the tensors alive until it is bound
     to others or closed, and those bound in a captured graph until it is closed; a captured graph needs the handle,
-    whose workspace it uses, and binds its list whenever it is replayed.  As with any torch call, tensors used on
-    another stream than the one they were allocated on must be kept until that stream is done with them."""
+    whose workspace it uses, until its last replay is done, and binds its list whenever it is replayed.  The workspace
+    may be used on any stream; as with any torch call, tensors used on another stream than the one they were allocated
+    on must be kept until that stream is done with them."""
 
     def __init__(self, tensors, out=None):
         self._tensors = list(tensors)
@@ -148,6 +149,7 @@ class ZeroGrads:
         self.h = None
         with torch.cuda.device(self.device):
             self.workspace = torch.empty(self.info.workspace_bytes, dtype=torch.uint8, device=self.device)
+            self._streams = {torch._C._cuda_getCurrentRawStream(self.device.index)}   # that the workspace knows of
             self.h = abi.zero_grads_init(desc, self.workspace.data_ptr(), self.info.workspace_bytes, self._stream())
         n = len(self._tensors)
         base = self.workspace.data_ptr()
@@ -188,7 +190,11 @@ class ZeroGrads:
         return dsts
 
     def _stream(self):
-        return torch._C._cuda_getCurrentRawStream(self.device.index)
+        stream = torch._C._cuda_getCurrentRawStream(self.device.index)
+        if stream not in self._streams:         # the workspace's memory is free when this one is done with it, too
+            self.workspace.record_stream(torch.cuda.current_stream(self.device))
+            self._streams.add(stream)
+        return stream
 
     def _capturing(self):
         if torch.cuda.current_device() == self.device.index:
