@@ -164,11 +164,6 @@ class ZeroError(RuntimeError):
         super().__init__(f"{fn} returned {status}: {msg}")
 
 
-def check(fn, status):
-    if status != ZERO_OK:
-        raise ZeroError(fn, status)
-
-
 def _call(name, *args):
     status = getattr(_lib or lib(), name)(*args)
     if status != ZERO_OK:
