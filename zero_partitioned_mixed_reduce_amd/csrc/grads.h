@@ -27,9 +27,9 @@ constexpr int kGradsWaves = kGradsBlock / 64;
 constexpr int kGradsRun = 4;
 // Bytes from one arrival counter to the next.  An arrival is done by the memory, and while many
 // of them meet in a few channels the reads of those channels wait: with counters 64 bytes apart
-// in groups of 256 blocks the norm of 1.56e9 bf16 elements takes 498 us, with 256 bytes 467, in
-// groups of 64 blocks 461; without any arrival the reads take 446.  512, 1024 and 4096 bytes
-// measured the same as 256.
+// in groups of 256 blocks the norm of 1.56e9 bf16 elements (without per-tensor norms, whose
+// arrivals add 13 us) takes 498 us, with 256 bytes 467, in groups of 64 blocks 461 to 465; without
+// any arrival the reads take 446.  512, 1024 and 4096 bytes measured the same as 256.
 #ifndef ZS_GRADS_PITCH
 #define ZS_GRADS_PITCH 256
 #endif

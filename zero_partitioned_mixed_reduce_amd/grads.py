@@ -108,8 +108,10 @@ class ZeroGrads:
     """Norm, clipping and scaling of one list of gradients.
 
     tensors: CUDA tensors of one device, fp16, bf16 or fp32 in any mixture; contiguous, or slices whose elements
-    form rows at one pitch.  out: None (in place), one tensor per gradient with as many elements, or one flat
-    contiguous tensor that takes them back to back in list order (e.g. a rank's buffer for zero_reduce_grads).
+    form rows at one pitch.  A parameter without a gradient is left out, or stands there as a tensor of zeros where
+    its place in a flat out has to be filled.  out: None (in place), one tensor per gradient with as many elements,
+    or one flat contiguous tensor that takes them back to back in list order (e.g. a rank's buffer for
+    zero_reduce_grads).
     The tensors' addresses are the plan's; zero_grads_bind gives new ones.
 
     After a norm, `norm` (0-dim) and, with per_tensor, `norms` [n] are fp32 device tensors in the workspace,
