@@ -302,3 +302,24 @@ def test_workspace_of_a_handle_closed_while_another_stream_works():
     for o, g in zip(keep, grads):
         want = g.double() * coef
         assert ((o.double() - want).abs() <= 4 * H * want.abs() + 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("sizes", [(5000, 0, 700), (0, 0)])
+def test_a_captured_clip_has_not_run(sizes):
+    """There is nothing to query before the first replay; afterwards every replay gives what the eager call gives."""
+    grads = [rand(i, n, torch.float32) for i, n in enumerate(sizes)]
+    h = ZeroGrads(grads, out=[torch.empty_like(g) for g in grads])
+    g = captured(lambda: h.zero_grads_clip_norm(1e-3, scope=EACH))
+    with pytest.raises(ZeroError) as e:
+        h.query()
+    assert e.value.status == _abi.ZERO_ESTATE
+    for step in range(3):
+        for i, x in enumerate(grads):
+            x.copy_(rand(10 * step + i, x.numel(), torch.float32))
+        h.tensor_acc.fill_(9.0)
+        g.replay()
+        q, each, out = h.query(), h.tensor_acc.clone(), [o.clone() for o in h._out]
+        check_norms(h, grads, L2, 1.0)
+        h.zero_grads_clip_norm(1e-3, scope=EACH)
+        assert h.query() == q and torch.equal(h.tensor_acc, each)
+        assert all((bits(a) == bits(b)).all() for a, b in zip(out, h._out))

@@ -9,8 +9,8 @@
 // (global loads take any), so tensors that lie back to back at odd offsets need no slow path.
 //
 // Measured (MI355X; a copy reaches 6.4 TB/s, pure reads 7.1): norm of 1.56e9 bf16 elements with
-// per-tensor norms 478 us, 6.5 TB/s, without 465; scaling them into another buffer 1012 us, 6.1 TB/s, and 4.1e8 fp32
-// elements into bf16 361 us, 6.7 TB/s.
+// per-tensor norms 478 us, 6.5 TB/s, without 465; scaling them into another buffer 1012 us,
+// 6.1 TB/s, and 4.1e8 fp32 elements into bf16 361 us, 6.7 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -526,8 +526,9 @@ __device__ void norm_block_end(typename Acc<KIND>::V item, int n_items, int firs
 // arrival -- is paid once for them, or a wave item per wave.  Items that go on with one run of
 // elements are streamed as one; the first of them has their sum, the others nothing.  Only the
 // first wave stays for the end; the others leave their places to the blocks that wait.  The norm
-// of 1.56e9 bf16 elements (with per-tensor norms) takes 524 us in runs of one item, 488 of 2, 477 of 4, 473 of 8 and 470
-// of 16; the clip of 1.2e8 124, 124, 124, 134 and 129 (few blocks, and the last ones alone).
+// of 1.56e9 bf16 elements (with per-tensor norms) takes 524 us in runs of one item, 488 of 2, 477
+// of 4, 473 of 8 and 470 of 16; the clip of 1.2e8 124, 124, 124, 134 and 129 (few blocks, and the
+// last ones alone).
 template <int KIND, bool NT>
 __global__ void __launch_bounds__(kGradsBlock, 7) grads_norm_kernel(GradsArgs a, float inv, int per_tensor,
                                                                  ClipArgs clip) {

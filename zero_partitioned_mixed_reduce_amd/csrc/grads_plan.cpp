@@ -229,8 +229,8 @@ zero_status_t build_grads_plan(const zero_grads_tensor_t* tensors, int64_t n, Gr
   p.norm_grid = (n_block + p.run - 1) / p.run + n_wave_blocks;
   // Groups of about the square root of the blocks, at most 64: every arrival on one counter
   // takes about 10 ns, so groups of 256 made the norm of 4.2e6 bf16 elements (512 blocks) 9.1 us,
-  // groups of 64 6.7.  1.56e9 elements (no per-tensor norms) take 467 us in groups of 256, 461 of 64, 506 of 16, whose
-  // own arrivals crowd the top.  Up to 128 blocks one group is as fast as a second level.
+  // groups of 64 6.7.  1.56e9 elements (without per-tensor norms) take 467 us in groups of 256,
+  // 461 of 64, 506 of 16, whose own arrivals crowd the top.  Up to 128 blocks one group is as fast as a second level.
   p.group = 128;
   if (p.norm_grid > 128)
     for (p.group = 16; p.group < 64 && p.group * p.group < p.norm_grid;) p.group *= 2;
