@@ -11,6 +11,9 @@ ZERO_OK, ZERO_EINVAL, ZERO_ENOMEM, ZERO_EHIP, ZERO_ESTATE = 0, -1, -2, -3, -4
 ZERO_F16, ZERO_BF16, ZERO_F32 = 1, 2, 3
 ZERO_NORM_L2, ZERO_NORM_MAX = 1, 2
 ZERO_CLIP_GLOBAL, ZERO_CLIP_EACH = 1, 2
+ZERO_SCALE_POW2, ZERO_SCALE_MAX = 1, 2
+ZERO_ACT_GELU, ZERO_ACT_SILU = 1, 2
+ZERO_PACKED_LINEAR, ZERO_PACKED_WEIGHT_GRAD, ZERO_PACKED_INPUT_GRAD = 1, 2, 3
 ZERO_ACCUMULATED = -1
 ZERO_DEVICE_LOSS_SCALE = 0.0
 ZERO_STATIC_WORKSPACE_BYTES = 8 * 1024 * 1024
@@ -70,6 +73,18 @@ class zero_grads_info_t(ctypes.Structure):
         return {n: getattr(self, n) for n, _ in self._fields_}
 
 
+class zero_matrix_t(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("pitch", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
+
+
+class zero_packed_t(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("pitch", ctypes.c_int64), ("rule", ctypes.c_int32)]
+
+
+_matrix_p, _packed_p = ctypes.POINTER(zero_matrix_t), ctypes.POINTER(zero_packed_t)
+
 _PROTOS = {
     "zero_shard_plan": [ctypes.POINTER(zero_shard_desc_t), ctypes.POINTER(zero_shard_info_t)],
     "zero_shard_init": [ctypes.POINTER(zero_shard_desc_t), ctypes.POINTER(zero_shard_bufs_t), ctypes.c_void_p,
@@ -120,6 +135,17 @@ _PROTOS = {
     "zero_grads_query": [ctypes.c_void_p, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int32),
                          ctypes.POINTER(ctypes.c_float), ctypes.c_void_p],
     "zero_grads_destroy": [ctypes.c_void_p],
+    # packed rows, include/zero_packed.h
+    "zero_packed_write": [_matrix_p, _packed_p, ctypes.c_void_p],
+    "zero_packed_read": [_packed_p, _matrix_p, ctypes.c_void_p],
+    "zero_packed_workspace": [ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, c_i64p],
+    "zero_packed_linear": [_packed_p, _packed_p, _matrix_p, _matrix_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p],
+    "zero_packed_weight_grad": [_matrix_p, _packed_p, _matrix_p, _matrix_p, ctypes.c_int32, ctypes.c_void_p,
+                                ctypes.c_int64, ctypes.c_void_p],
+    "zero_packed_input_grad": [_matrix_p, _packed_p, _matrix_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64,
+                               ctypes.c_void_p],
+    "zero_packed_act": [ctypes.c_int32, ctypes.c_int32, _matrix_p, _packed_p, _matrix_p, _packed_p, ctypes.c_void_p],
+    "zero_packed_act_grad": [ctypes.c_int32, ctypes.c_int32, _packed_p, _matrix_p, _matrix_p, ctypes.c_void_p],
     # offloaded (host) step, include/zero_offload.h
     "zero_offload_init": [ctypes.POINTER(zero_shard_desc_t), ctypes.POINTER(zero_offload_bufs_t), ctypes.c_void_p,
                           ctypes.c_int32, ctypes.c_void_p, ctypes.POINTER(ctypes.c_void_p)],
@@ -364,6 +390,41 @@ def zero_grads_query(h, stream):
 
 def zero_grads_destroy(h):
     _call("zero_grads_destroy", h)
+
+
+def zero_packed_write(x, p, stream):
+    """Here and below: x, y, dy, dw, db, dx and bias are zero_matrix_t, packed rows zero_packed_t; None for NULL."""
+    _call("zero_packed_write", x, p, stream)
+
+
+def zero_packed_read(p, out, stream):
+    _call("zero_packed_read", p, out, stream)
+
+
+def zero_packed_workspace(call, m, k, n):
+    b = ctypes.c_int64()
+    _call("zero_packed_workspace", call, m, k, n, ctypes.byref(b))
+    return b.value
+
+
+def zero_packed_linear(x, w, bias, y, workspace_ptr, workspace_capacity, stream):
+    _call("zero_packed_linear", x, w, bias, y, workspace_ptr, workspace_capacity, stream)
+
+
+def zero_packed_weight_grad(dy, x, dw, db, accumulate, workspace_ptr, workspace_capacity, stream):
+    _call("zero_packed_weight_grad", dy, x, dw, db, int(bool(accumulate)), workspace_ptr, workspace_capacity, stream)
+
+
+def zero_packed_input_grad(dy, w, dx, accumulate, workspace_ptr, workspace_capacity, stream):
+    _call("zero_packed_input_grad", dy, w, dx, int(bool(accumulate)), workspace_ptr, workspace_capacity, stream)
+
+
+def zero_packed_act(kind, gated, x, xp, y, yp, stream):
+    _call("zero_packed_act", kind, int(bool(gated)), x, xp, y, yp, stream)
+
+
+def zero_packed_act_grad(kind, gated, xp, dy, dx, stream):
+    _call("zero_packed_act_grad", kind, int(bool(gated)), xp, dy, dx, stream)
 
 
 def zero_offload_init(desc, bufs, master_init_ptr, num_threads, stream):

@@ -1,0 +1,515 @@
+// gfx950 kernels of the packed rows' products: the linear layer in 8-bit integers, and the products
+// of a 16-bit matrix with packed rows whose scales lie along the sum (weight and input gradients).
+#include <type_traits>
+
+#include "packed_device.h"
+
+namespace zs {
+namespace packed {
+
+#define ZS_LDS(T) __attribute__((address_space(3))) T
+
+constexpr int kXcds = 8;  // consecutive blocks go to the XCDs in turn, each with an L2 cache of its own
+
+// The tile of block b: each XCD takes a run of consecutive tiles, and a run goes down kDown tiles of
+// i before it steps to the next j, so that what an XCD works on at a time shares rows and columns.
+constexpr int kDown = 8;
+struct Tile {
+  int64_t i, j;
+};
+__device__ __forceinline__ Tile tile_of(uint32_t b, uint32_t ni, uint32_t nj) {
+  const uint32_t n = ni * nj, per = n / kXcds, more = n % kXcds, x = b % kXcds;
+  const uint32_t t = x * per + (x < more ? x : more) + b / kXcds;
+  const uint32_t band = t / (kDown * nj), in = t % (kDown * nj);
+  const uint32_t high = ni - band * kDown < kDown ? ni - band * kDown : kDown;
+  return {band * kDown + in % high, in / high};
+}
+
+__device__ __forceinline__ float load1(const MatArg& a, int64_t at) {
+  if (a.dtype == ZERO_F32) return ((const float*)a.p)[at];
+  const uint32_t h = ((const uint16_t*)a.p)[at];
+  return a.dtype == ZERO_BF16 ? dec_lo<ZERO_BF16>(h) : dec_lo<ZERO_F16>(h);
+}
+// Four consecutive results of a row, those before column n, into a matrix of any type.
+__device__ __forceinline__ void store4(const MatArg& c, int64_t r, int64_t col, int64_t n, const float (&x)[4]) {
+  const int64_t at = r * c.pitch + col;
+  if (c.vec && col + 4 <= n) {
+    if (c.dtype == ZERO_F32) *(f32x4*)((float*)c.p + at) = f32x4{x[0], x[1], x[2], x[3]};
+    else if (c.dtype == ZERO_BF16) *(u32x2*)((uint16_t*)c.p + at) = u32x2{enc2<ZERO_BF16>(x[0], x[1]), enc2<ZERO_BF16>(x[2], x[3])};
+    else *(u32x2*)((uint16_t*)c.p + at) = u32x2{enc2<ZERO_F16>(x[0], x[1]), enc2<ZERO_F16>(x[2], x[3])};
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (col + i < n) {
+      if (c.dtype == ZERO_F32) ((float*)c.p)[at + i] = x[i];
+      else if (c.dtype == ZERO_BF16) ((uint16_t*)c.p)[at + i] = (uint16_t)enc2<ZERO_BF16>(x[i], 0.0f);
+      else ((uint16_t*)c.p)[at + i] = (uint16_t)enc2<ZERO_F16>(x[i], 0.0f);
+    }
+}
+__device__ __forceinline__ void load4(const MatArg& c, int64_t r, int64_t col, int64_t n, float (&x)[4]) {
+  const int64_t at = r * c.pitch + col;
+  if (c.vec && col + 4 <= n) {
+    if (c.dtype == ZERO_F32) {
+      const f32x4 v = *(const f32x4*)((const float*)c.p + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = v[i];
+    } else {
+      const u32x2 v = *(const u32x2*)((const uint16_t*)c.p + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[i] = c.dtype == ZERO_BF16 ? ((i & 1) ? dec_hi<ZERO_BF16>(v[i >> 1]) : dec_lo<ZERO_BF16>(v[i >> 1]))
+                                    : ((i & 1) ? dec_hi<ZERO_F16>(v[i >> 1]) : dec_lo<ZERO_F16>(v[i >> 1]));
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = col + i < n ? load1(c, at + i) : 0.0f;
+}
+
+// ---------------------------------------------------------------------------
+// Linear layer: y[m][n] = sum over k of x[m][k] w[n][k], 16x16x64 integer matrix instructions.
+
+constexpr int kStepK = 128;  // k of a tile step: a row of 128 bytes
+
+// What a sum becomes.
+struct LinearOut {
+  float ws[4], b[4];
+};
+__device__ __forceinline__ void linear_store(const LinearArgs& a, int64_t m, int64_t n, const i32x4& acc, float xs,
+                                             const float (&ws)[4], const float (&b)[4]) {
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = (float)acc[i] * xs * ws[i];
+    if (a.bias.p) v[i] += b[i];
+  }
+  store4(a.y, m, n, a.n, v);
+}
+__device__ __forceinline__ void channel4(const LinearArgs& a, int64_t n, float (&ws)[4], float (&b)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    ws[i] = n + i < a.n ? a.w.scale[n + i] : 0.0f;
+    b[i] = a.bias.p && n + i < a.n ? load1(a.bias, n + i) : 0.0f;
+  }
+}
+
+template <int BM, int BN, int WM, int WN>
+__global__ void __launch_bounds__(WM* WN * 64) linear_kernel(LinearArgs a, uint32_t tiles_m, uint32_t tiles_n, int64_t steps,
+                                                            int64_t per_split) {
+  constexpr int W = WM * WN, T = W * 64;
+  constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16x16 results of a wave
+  constexpr int LX = BM * 8 / T, LW = BN * 8 / T;      // 16-byte loads of a thread
+  static_assert(BM * 8 % T == 0 && BN * 8 % T == 0, "whole loads");
+  __shared__ __attribute__((aligned(1024))) char lds[2][(BM + BN) * kStepK];
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const Tile tile = tile_of(blockIdx.x, tiles_m, tiles_n);
+  const int64_t m0 = tile.i * BM, n0 = tile.j * BN;
+  const int64_t first = (int64_t)blockIdx.y * per_split, last = first + per_split < steps ? first + per_split : steps;
+  const int chunks = (int)((a.k + 15) >> 4);  // 16-byte chunks of a row
+
+  // A wave's load fills 8 rows of 128 bytes; chunk c of row r lies in place c ^ (r / 2 % 8), so that
+  // the sixteen rows a fragment read takes at one k lie in different banks.  Rows past the end read
+  // the last one, and their results are not stored.
+  const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(a.x.q + m0 * a.x.pitch, 0, 0xFFFFFFFFu, 0x00020000);
+  const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(a.w.q + n0 * a.w.pitch, 0, 0xFFFFFFFFu, 0x00020000);
+  const int mlast = (int)(a.m - 1 - m0 < BM - 1 ? a.m - 1 - m0 : BM - 1);
+  const int nlast = (int)(a.n - 1 - n0 < BN - 1 ? a.n - 1 - n0 : BN - 1);
+  const auto fill = [&](int buf, int64_t step) __attribute__((always_inline)) {
+    const int c0 = (int)step * 8;
+#pragma unroll
+    for (int u = 0; u < LX + LW; ++u) {
+      const int r = ((u < LX ? u : u - LX) * W + wave) * 8 + (lane >> 3);
+      const int edge = u < LX ? mlast : nlast;
+      int c = c0 + ((lane & 7) ^ ((r >> 1) & 7));
+      c = c < chunks ? c : chunks - 1;
+      const uint32_t at = (uint32_t)(r < edge ? r : edge) * (uint32_t)(u < LX ? a.x.pitch : a.w.pitch) + (uint32_t)c * 16u;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(u < LX ? xr : wr, (ZS_LDS(void)*)(&lds[buf][(u * W + wave) * 1024]), 16, at, 0, 0, 0);
+    }
+  };
+
+  const int wm = wave / WN, wn = wave % WN;
+  const int l16 = lane & 15, l4 = lane >> 4;
+  const int xrow = (wm * TM * 16 + l16) * kStepK, wrow = (BM + wn * TN * 16 + l16) * kStepK;
+  i32x4 acc[TM][TN] = {};
+  const auto compute = [&](int buf, int left) __attribute__((always_inline)) {  // left: chunks of the row from here on
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      const int place = ((ks * 4 + l4) ^ (l16 >> 1)) * 16;
+      i32x4 xf[TM], wf[TN];
+#pragma unroll
+      for (int i = 0; i < TM; ++i) xf[i] = *(const i32x4*)(&lds[buf][xrow + i * 16 * kStepK + place]);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        wf[j] = *(const i32x4*)(&lds[buf][wrow + j * 16 * kStepK + place]);
+        if (left < 8 && ks * 4 + l4 >= left) wf[j] = i32x4{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[j], xf[i], acc[i][j], 0, 0, 0);
+    }
+  };
+
+  if (first < last) fill(0, first);
+  int buf = 0;
+  for (int64_t s = first; s < last; ++s) {
+    __syncthreads();  // this step's loads are done, and nobody reads the other buffer any more
+    if (s + 1 < last) fill(buf ^ 1, s + 1);
+    compute(buf, chunks - (int)s * 8);
+    buf ^= 1;
+  }
+
+  // results: row n0 + 4 (lane / 16) + element, column m0 + lane % 16 of each 16x16
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    const int64_t n = n0 + wn * TN * 16 + j * 16 + l4 * 4;
+    float ws[4], b[4];
+    if (n >= a.n) continue;
+    if (!a.part) channel4(a, n, ws, b);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int64_t m = m0 + wm * TM * 16 + i * 16 + l16;
+      if (m >= a.m) continue;
+      if (a.part) *(i32x4*)(a.part + ((int64_t)blockIdx.y * a.m + m) * a.n4 + n) = acc[i][j];
+      else linear_store(a, m, n, acc[i][j], a.x.scale[m], ws, b);
+    }
+  }
+}
+
+// Adds the splits' integer sums, which no order changes.
+__global__ void __launch_bounds__(256) linear_join_kernel(LinearArgs a, int splits) {
+  const int64_t quads = a.n4 / 4;
+  for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < a.m * quads; q += (int64_t)gridDim.x * 256) {
+    const int64_t m = q / quads, n = q % quads * 4;
+    i32x4 acc = {0, 0, 0, 0};
+    for (int s = 0; s < splits; ++s) acc += *(const i32x4*)(a.part + ((int64_t)s * a.m + m) * a.n4 + n);
+    float ws[4], b[4];
+    channel4(a, n, ws, b);
+    linear_store(a, m, n, acc, a.x.scale[m], ws, b);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Gradients: c[i][j] = sum over s of a[s][i] (or a[i][s]) scale[s] q[s][j], 16x16x32 bf16 matrix
+// instructions.  Tiles lie in LDS as [s][..] (or [i][s]); the instruction wants each lane's
+// values along s, which the transposing LDS read gives.
+
+constexpr int kStepC = 64;
+
+// Place of 16-element segment g of row s in a tile [s][...]: the rows that a transposing read takes
+// together lie in different banks.
+__device__ __forceinline__ int seg_swizzle(int s) { return (s & 3) | ((s >> 1) & 4); }
+
+// Splits v into two bf16 values whose sum is v to 16 bits (exactly, if it has no more).
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+  const float ha = dec_lo<ZERO_BF16>(hi), hb = dec_hi<ZERO_BF16>(hi);
+  // nothing is left of an infinity
+  const float ra = __builtin_isinf(ha) ? 0.0f : a - ha, rb = __builtin_isinf(hb) ? 0.0f : b - hb;
+  lo = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{ra, rb}), bf16x2));
+}
+
+// TWO: the scales go into a, whose values then take two bf16 terms; else into q's, exactly.
+template <int DT, bool TRANS, bool TWO, int BI, int BJ, int WI, int WJ>
+__global__ void __launch_bounds__(WI* WJ * 64) grad_kernel(GradArgs g, uint32_t tiles_i, uint32_t tiles_j, int64_t steps,
+                                                          int64_t per_split) {
+  constexpr int T = WI * WJ * 64, S = kStepC;
+  constexpr int TI = BI / WI / 16, TJ = BJ / WJ / 16;
+  constexpr int LA = BI * S / 8 / T, LQ = BJ * S / 16 / T;  // chunks of a thread
+  constexpr int ABYTES = BI * S * 2, TERMS = TWO ? 2 : 1;
+  static_assert(BI * S / 8 % T == 0 && BJ * S / 16 % T == 0, "whole chunks");
+  __shared__ __attribute__((aligned(1024))) char lds[2][ABYTES * TERMS + BJ * S * 2];
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const Tile tile = tile_of(blockIdx.x, tiles_i, tiles_j);
+  const int64_t i0 = tile.i * BI, j0 = tile.j * BJ;
+  const int64_t first = (int64_t)blockIdx.y * per_split, last = first + per_split < steps ? first + per_split : steps;
+
+  Raw8<ZERO_BF16> ra[LA];
+  u32x4 rq[LQ];
+  float rs[TWO ? (TRANS ? LA : 1) : LQ];
+  float rs8[TWO && !TRANS ? LA : 1][8];
+  const auto fetch = [&](int64_t step) __attribute__((always_inline)) {
+    const int64_t s0 = step * S;
+#pragma unroll
+    for (int u = 0; u < LA; ++u) {
+      const int id = u * T + t;
+      if constexpr (TRANS) {
+        const int64_t s = s0 + id / (BI / 8), i = i0 + id % (BI / 8) * 8;
+        const bool in = s < g.nc;
+        ra[u] = load8<ZERO_BF16>((const char*)g.a.p + (in ? s : 0) * g.a.pitch * 2, i, in ? g.ni : 0);
+        if constexpr (TWO) rs[u] = in ? g.q.scale[s] : 0.0f;
+      } else {
+        const int64_t i = i0 + id / (S / 8), s = s0 + id % (S / 8) * 8;
+        const bool in = i < g.ni;
+        ra[u] = load8<ZERO_BF16>((const char*)g.a.p + (in ? i : 0) * g.a.pitch * 2, s, in ? g.nc : 0);
+        if constexpr (TWO) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) rs8[u][k] = s + k < g.nc ? g.q.scale[s + k] : 0.0f;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < LQ; ++u) {
+      const int id = u * T + t;
+      const int64_t s = s0 + id / (BJ / 16), j = j0 + id % (BJ / 16) * 16;
+      const bool in = s < g.nc && j < g.nj;
+      rq[u] = in ? *(const u32x4*)(g.q.q + s * g.q.pitch + j) : u32x4{0, 0, 0, 0};
+      if constexpr (!TWO) rs[u] = in ? g.q.scale[s] : 0.0f;
+    }
+  };
+  const auto stage = [&](int buf) __attribute__((always_inline)) {
+    char* la = lds[buf];
+    char* lq = lds[buf] + ABYTES * TERMS;
+#pragma unroll
+    for (int u = 0; u < LA; ++u) {
+      const int id = u * T + t;
+      int at;
+      if constexpr (TRANS) {
+        const int s = id / (BI / 8), c = id % (BI / 8);
+        at = s * BI * 2 + (((c >> 1) ^ seg_swizzle(s)) << 5) + (c & 1) * 16;
+      } else {
+        const int i = id / (S / 8), c = id % (S / 8);
+        at = i * S * 2 + ((c ^ ((i >> 1) & 7)) << 4);
+      }
+      if constexpr (TWO) {
+        u32x4 hi, lo;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float s0 = TRANS ? rs[TRANS ? u : 0] : rs8[TRANS ? 0 : u][2 * k], s1 = TRANS ? rs[TRANS ? u : 0] : rs8[TRANS ? 0 : u][2 * k + 1];
+          uint32_t h, l;
+          split2(dec_lo<DT>(ra[u].v[0][k]) * s0, dec_hi<DT>(ra[u].v[0][k]) * s1, h, l);
+          hi[k] = h;
+          lo[k] = l;
+        }
+        *(u32x4*)(la + at) = hi;
+        *(u32x4*)(la + ABYTES + at) = lo;
+      } else {
+        *(u32x4*)(la + at) = ra[u].v[0];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < LQ; ++u) {
+      const int id = u * T + t;
+      const int s = id / (BJ / 16), c = id % (BJ / 16);
+      char* to = lq + s * BJ * 2 + ((c ^ seg_swizzle(s)) << 5);
+      const float scale = TWO ? 1.0f : rs[TWO ? 0 : u];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        u32x4 o;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t w = rq[u][2 * h + (k >> 1)];
+          const f32x2 v = {q_of(w, (k & 1) * 2) * scale, q_of(w, (k & 1) * 2 + 1) * scale};
+          o[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+        }
+        *(u32x4*)(to + 16 * h) = o;
+      }
+    }
+  };
+
+  const int wi = wave / WJ, wj = wave % WJ;
+  const int l16 = lane & 15, l4 = lane >> 4;
+  // a transposing read takes, in each sixteen lanes, four rows of sixteen columns
+  const int trow = l4 * 8 + (l16 >> 2), tcol = (l16 & 3) * 8, tswz = seg_swizzle(trow);
+  f32x4 acc[TI][TJ] = {};
+  const auto frag_t = [&](const char* base, int width, int seg, int ks) __attribute__((always_inline)) {
+    const char* p = base + trow * width * 2 + ((seg ^ tswz) << 5) + tcol + ks * 32 * width * 2;
+    const bf16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((ZS_LDS(bf16x4)*)p);
+    const bf16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((ZS_LDS(bf16x4)*)(p + 4 * width * 2));
+    return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  const auto compute = [&](int buf) __attribute__((always_inline)) {
+    const char* la = lds[buf];
+    const char* lq = lds[buf] + ABYTES * TERMS;
+#pragma unroll
+    for (int ks = 0; ks < S / 32; ++ks) {
+      bf16x8 qf[TJ];
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) qf[j] = frag_t(lq, BJ, wj * TJ + j, ks);
+#pragma unroll
+      for (int h = 0; h < TERMS; ++h) {
+        bf16x8 af[TI];
+#pragma unroll
+        for (int i = 0; i < TI; ++i) {
+          if constexpr (TRANS) {
+            af[i] = frag_t(la + h * ABYTES, BI, wi * TI + i, ks);
+          } else {
+            const int row = (wi * TI + i) * 16 + l16;
+            af[i] = *(const bf16x8*)(la + h * ABYTES + row * S * 2 + (((ks * 4 + l4) ^ (l16 >> 1)) << 4));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+#pragma unroll
+          for (int j = 0; j < TJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf[j], af[i], acc[i][j], 0, 0, 0);
+      }
+    }
+  };
+
+  if (first < last) {
+    fetch(first);
+    stage(0);
+  }
+  int buf = 0;
+  for (int64_t s = first; s < last; ++s) {
+    __syncthreads();
+    if (s + 1 < last) fetch(s + 1);
+    compute(buf);
+    if (s + 1 < last) stage(buf ^ 1);
+    buf ^= 1;
+  }
+
+#pragma unroll
+  for (int i = 0; i < TI; ++i) {
+    const int64_t r = i0 + (wi * TI + i) * 16 + l16;
+    if (r >= g.ni) continue;
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      const int64_t c = j0 + (wj * TJ + j) * 16 + l4 * 4;
+      if (c >= g.nj) continue;
+      if (g.part) {
+        *(f32x4*)(g.part + ((int64_t)blockIdx.y * g.ni + r) * g.nj4 + c) = acc[i][j];
+        continue;
+      }
+      float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+      if (g.accumulate) {
+        float old[4];
+        load4(g.c, r, c, g.nj, old);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] += old[k];
+      }
+      store4(g.c, r, c, g.nj, v);
+    }
+  }
+}
+
+// Adds the splits' sums, in their order.
+__global__ void __launch_bounds__(256) grad_join_kernel(GradArgs g, int splits) {
+  const int64_t quads = g.nj4 / 4;
+  for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < g.ni * quads; q += (int64_t)gridDim.x * 256) {
+    const int64_t r = q / quads, c = q % quads * 4;
+    f32x4 acc = {0, 0, 0, 0};
+    for (int s = 0; s < splits; ++s) acc += *(const f32x4*)(g.part + ((int64_t)s * g.ni + r) * g.nj4 + c);
+    float v[4] = {acc[0], acc[1], acc[2], acc[3]};
+    if (g.accumulate) {
+      float old[4];
+      load4(g.c, r, c, g.nj, old);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] += old[k];
+    }
+    store4(g.c, r, c, g.nj, v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Column sums: a block takes 512 columns (eight to a lane) and a run of rows, its waves every fourth.
+
+template <int DT>
+__global__ void __launch_bounds__(256) columns_kernel(MatArg dy, int64_t m, int64_t n, int64_t run, float* part) {
+  __shared__ float lds[4][512];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 512 + lane * 8;
+  const int64_t r0 = (int64_t)blockIdx.y * run, r1 = r0 + run < m ? r0 + run : m;
+  float s[8] = {};
+  for (int64_t r = r0 + wave; r < r1; r += 4) {
+    const Raw8<DT> x = load8<DT>((const char*)dy.p + r * dy.pitch * 2, c, n);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] += get<DT>(x, i);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) lds[wave][lane * 8 + i] = s[i];
+  __syncthreads();
+  for (int k = threadIdx.x; k < 512; k += 256) {
+    const int64_t col = (int64_t)blockIdx.x * 512 + k;
+    if (col < n) part[(int64_t)blockIdx.y * n + col] = (lds[0][k] + lds[1][k]) + (lds[2][k] + lds[3][k]);
+  }
+}
+__global__ void __launch_bounds__(256) columns_join_kernel(const float* part, int splits, int64_t n, MatArg db, int accumulate) {
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (c >= n) return;
+  float s = 0.0f;
+  for (int k = 0; k < splits; ++k) s += part[(int64_t)k * n + c];
+  if (accumulate) s += load1(db, c);
+  if (db.dtype == ZERO_F32) ((float*)db.p)[c] = s;
+  else if (db.dtype == ZERO_BF16) ((uint16_t*)db.p)[c] = (uint16_t)enc2<ZERO_BF16>(s, 0.0f);
+  else ((uint16_t*)db.p)[c] = (uint16_t)enc2<ZERO_F16>(s, 0.0f);
+}
+
+}  // namespace packed
+
+using namespace packed;
+
+static int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+static int64_t join_grid(int64_t quads) {
+  const int64_t b = up(quads, 256);
+  return b < 4096 ? b : 4096;
+}
+
+// Tiles of `bi` x `bj` and a contraction of `steps`: split until the chip's 256 compute units have a
+// block each, but no finer than four steps to a split.
+static ProductPlan plan_product(int64_t ni, int64_t nj, int64_t steps, int64_t bi, int64_t bj, int64_t elem) {
+  ProductPlan p{};
+  p.tiles_i = up(ni, bi);
+  p.tiles_j = up(nj, bj);
+  p.steps = steps;
+  const int64_t tiles = p.tiles_i * p.tiles_j;
+  int64_t s = tiles > 0 ? 256 / tiles : 1;
+  if (s > steps / 4) s = steps / 4;
+  if (s < 1) s = 1;
+  p.splits = up(steps > 0 ? steps : 1, up(steps > 0 ? steps : 1, s));
+  p.ws_bytes = p.splits > 1 ? p.splits * ni * (up(nj, 4) * 4) * elem : 0;
+  return p;
+}
+
+ProductPlan plan_linear(int64_t m, int64_t k, int64_t n) { return plan_product(m, n, up(k, kStepK), 128, 128, 4); }
+
+hipError_t launch_linear(const LinearArgs& a, const ProductPlan& p, hipStream_t st) {
+  const dim3 grid((uint32_t)(p.tiles_i * p.tiles_j), (uint32_t)p.splits);
+  linear_kernel<128, 128, 2, 2><<<grid, 256, 0, st>>>(a, (uint32_t)p.tiles_i, (uint32_t)p.tiles_j, p.steps, up(p.steps, p.splits));
+  if (a.part) linear_join_kernel<<<(uint32_t)join_grid(a.m * a.n4 / 4), 256, 0, st>>>(a, (int)p.splits);
+  return hipGetLastError();
+}
+
+ProductPlan plan_grad(int64_t ni, int64_t nj, int64_t nc) { return plan_product(ni, nj, up(nc, kStepC), 128, 128, 4); }
+
+template <int DT, bool TRANS, bool TWO>
+static void launch_grad_typed(const GradArgs& g, const ProductPlan& p, hipStream_t st) {
+  const dim3 grid((uint32_t)(p.tiles_i * p.tiles_j), (uint32_t)p.splits);
+  grad_kernel<DT, TRANS, TWO, 128, 128, 2, 2><<<grid, 256, 0, st>>>(g, (uint32_t)p.tiles_i, (uint32_t)p.tiles_j, p.steps, up(p.steps, p.splits));
+}
+
+hipError_t launch_grad(const GradArgs& g, bool trans, const ProductPlan& p, hipStream_t st) {
+  const bool two = g.a.dtype != ZERO_BF16 || g.q.rule != ZERO_SCALE_POW2;
+  if (g.a.dtype == ZERO_BF16) {
+    if (two) trans ? launch_grad_typed<ZERO_BF16, true, true>(g, p, st) : launch_grad_typed<ZERO_BF16, false, true>(g, p, st);
+    else trans ? launch_grad_typed<ZERO_BF16, true, false>(g, p, st) : launch_grad_typed<ZERO_BF16, false, false>(g, p, st);
+  } else {
+    trans ? launch_grad_typed<ZERO_F16, true, true>(g, p, st) : launch_grad_typed<ZERO_F16, false, true>(g, p, st);
+  }
+  if (g.part) grad_join_kernel<<<(uint32_t)join_grid(g.ni * g.nj4 / 4), 256, 0, st>>>(g, (int)p.splits);
+  return hipGetLastError();
+}
+
+ColumnsPlan plan_columns(int64_t m, int64_t n) {
+  ColumnsPlan p;
+  const int64_t wide = up(n > 0 ? n : 1, 512);
+  int64_t s = up(1024, wide);
+  if (s > up(m, 32)) s = up(m, 32);
+  if (s < 1) s = 1;
+  p.run = up(m > 0 ? m : 1, s);
+  p.splits = up(m > 0 ? m : 1, p.run);
+  p.ws_bytes = p.splits * n * 4;
+  return p;
+}
+
+hipError_t launch_columns(const MatArg& dy, int64_t m, int64_t n, const MatArg& db, bool accumulate, float* part,
+                          const ColumnsPlan& p, hipStream_t st) {
+  const dim3 grid((uint32_t)up(n, 512), (uint32_t)p.splits);
+  if (dy.dtype == ZERO_BF16) columns_kernel<ZERO_BF16><<<grid, 256, 0, st>>>(dy, m, n, p.run, part);
+  else columns_kernel<ZERO_F16><<<grid, 256, 0, st>>>(dy, m, n, p.run, part);
+  columns_join_kernel<<<(uint32_t)up(n, 256), 256, 0, st>>>(part, (int)p.splits, n, db, accumulate);
+  return hipGetLastError();
+}
+
+}  // namespace zs
