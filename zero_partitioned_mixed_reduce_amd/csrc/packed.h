@@ -7,13 +7,11 @@
 
 namespace zs {
 
-// A matrix in floating point.  vec: four consecutive elements from a column that is a multiple of
-// four lie on their own size's boundary, in every row.
+// A matrix in floating point.
 struct MatArg {
   void* p;
   int64_t pitch;  // elements
   int32_t dtype;
-  int32_t vec;
 };
 
 // Packed rows.
@@ -30,7 +28,7 @@ struct ProductPlan {
   int64_t tiles_i, tiles_j;
   int64_t steps, splits;
   int64_t ws_bytes;
-  int32_t tile;  // index of the tile's shape
+  int32_t tile;  // rows of a tile
 };
 
 // y [m][n] of x [m][k] and w [n][k].

@@ -82,11 +82,7 @@ zero_status_t apart(const Span& out, const Span& in, const char* a, const char* 
   return meet(out, in) ? bad(std::string(a) + " shares memory with " + b) : ZERO_OK;
 }
 
-zs::MatArg arg(const zero_matrix_t& a) {
-  const int64_t s = esize(a.dtype);
-  const bool vec = (uintptr_t)a.data % (uintptr_t)(4 * s) == 0 && (a.rows <= 1 || a.pitch % 4 == 0);
-  return {a.data, a.rows > 1 ? a.pitch : a.cols, a.dtype, vec};
-}
+zs::MatArg arg(const zero_matrix_t& a) { return {a.data, a.rows > 1 ? a.pitch : a.cols, a.dtype}; }
 zs::PackArg arg(const zero_packed_t& p) { return {p.q, p.scale, p.pitch, p.rule}; }
 
 zero_status_t check_workspace(void* workspace, int64_t capacity, int64_t need, const Span* used, int n_used) {

@@ -30,151 +30,243 @@ __device__ __forceinline__ float load1(const MatArg& a, int64_t at) {
   const uint32_t h = ((const uint16_t*)a.p)[at];
   return a.dtype == ZERO_BF16 ? dec_lo<ZERO_BF16>(h) : dec_lo<ZERO_F16>(h);
 }
-// Four consecutive results of a row, those before column n, into a matrix of any type.
-__device__ __forceinline__ void store4(const MatArg& c, int64_t r, int64_t col, int64_t n, const float (&x)[4]) {
-  const int64_t at = r * c.pitch + col;
-  if (c.vec && col + 4 <= n) {
-    if (c.dtype == ZERO_F32) *(f32x4*)((float*)c.p + at) = f32x4{x[0], x[1], x[2], x[3]};
-    else if (c.dtype == ZERO_BF16) *(u32x2*)((uint16_t*)c.p + at) = u32x2{enc2<ZERO_BF16>(x[0], x[1]), enc2<ZERO_BF16>(x[2], x[3])};
-    else *(u32x2*)((uint16_t*)c.p + at) = u32x2{enc2<ZERO_F16>(x[0], x[1]), enc2<ZERO_F16>(x[2], x[3])};
-    return;
-  }
+// N consecutive elements of a row, those before column n (N = 4 or 16), at any alignment.
+template <int DT, int N>
+__device__ __forceinline__ void store_run(char* row, int64_t col, int64_t n, const float (&x)[N]) {
+  constexpr int S = esize(DT);
+  char* p = row + col * S;
+  uint32_t w[N * S / 4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (col + i < n) {
-      if (c.dtype == ZERO_F32) ((float*)c.p)[at + i] = x[i];
-      else if (c.dtype == ZERO_BF16) ((uint16_t*)c.p)[at + i] = (uint16_t)enc2<ZERO_BF16>(x[i], 0.0f);
-      else ((uint16_t*)c.p)[at + i] = (uint16_t)enc2<ZERO_F16>(x[i], 0.0f);
+  for (int i = 0; i < N * S / 4; ++i) {
+    if constexpr (DT == ZERO_F32) w[i] = __float_as_uint(x[i]);
+    else w[i] = enc2<DT>(x[2 * i], x[2 * i + 1]);
+  }
+  if (col + N <= n) {
+    constexpr int V = N * S / 4 < 4 ? N * S / 4 : 4;
+    typedef uint32_t vec __attribute__((ext_vector_type(V)));
+#pragma unroll
+    for (int i = 0; i < N * S / 4; i += V) {
+      vec v;
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[k] = w[i + k];
+      store_any(p + 4 * i, v);
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (col + i < n) {
+        if constexpr (DT == ZERO_F32) store_any(p + 4 * i, w[i]);
+        else store_any(p + 2 * i, (uint16_t)(w[i >> 1] >> (16 * (i & 1))));
+      }
+  }
 }
-__device__ __forceinline__ void load4(const MatArg& c, int64_t r, int64_t col, int64_t n, float (&x)[4]) {
-  const int64_t at = r * c.pitch + col;
-  if (c.vec && col + 4 <= n) {
-    if (c.dtype == ZERO_F32) {
-      const f32x4 v = *(const f32x4*)((const float*)c.p + at);
+template <int DT, int N>
+__device__ __forceinline__ void load_run(const char* row, int64_t col, int64_t n, float (&x)[N]) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = v[i];
+  for (int i = 0; i < N; i += 4) {
+    if (col + i + 4 <= n) {
+      if constexpr (DT == ZERO_F32) {
+        const f32x4 v = load_any<f32x4>(row + (col + i) * 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[i + k] = v[k];
+      } else {
+        const u32x2 v = load_any<u32x2>(row + (col + i) * 2);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[i + k] = (k & 1) ? dec_hi<DT>(v[k >> 1]) : dec_lo<DT>(v[k >> 1]);
+      }
     } else {
-      const u32x2 v = *(const u32x2*)((const uint16_t*)c.p + at);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        x[i] = c.dtype == ZERO_BF16 ? ((i & 1) ? dec_hi<ZERO_BF16>(v[i >> 1]) : dec_lo<ZERO_BF16>(v[i >> 1]))
-                                    : ((i & 1) ? dec_hi<ZERO_F16>(v[i >> 1]) : dec_lo<ZERO_F16>(v[i >> 1]));
+      for (int k = 0; k < 4; ++k) {
+        x[i + k] = 0.0f;
+        if (col + i + k < n) {
+          if constexpr (DT == ZERO_F32) x[i + k] = load_any<float>(row + (col + i + k) * 4);
+          else x[i + k] = dec_lo<DT>(load_any<uint16_t>(row + (col + i + k) * 2));
+        }
+      }
     }
-    return;
   }
+}
+// Calls fn with the type of a matrix, which is the same for a whole launch.
+template <class F>
+__device__ __forceinline__ void with_type(int32_t dt, F fn) {
+  if (dt == ZERO_BF16) fn(std::integral_constant<int, ZERO_BF16>());
+  else if (dt == ZERO_F16) fn(std::integral_constant<int, ZERO_F16>());
+  else fn(std::integral_constant<int, ZERO_F32>());
+}
+// N results of row r from column c, with what the matrix holds added if asked for.
+template <int DT, int N>
+__device__ __forceinline__ void finish_run(const MatArg& c, int64_t r, int64_t col, int64_t n, int32_t accumulate, float (&v)[N]) {
+  char* row = (char*)c.p + r * c.pitch * esize(DT);
+  if (accumulate) {
+    float old[N];
+    load_run<DT, N>(row, col, n, old);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = col + i < n ? load1(c, at + i) : 0.0f;
+    for (int k = 0; k < N; ++k) v[k] += old[k];
+  }
+  store_run<DT, N>(row, col, n, v);
 }
 
 // ---------------------------------------------------------------------------
 // Linear layer: y[m][n] = sum over k of x[m][k] w[n][k], 16x16x64 integer matrix instructions.
 
-constexpr int kStepK = 128;  // k of a tile step: a row of 128 bytes
+constexpr int kStepK = 64;  // k of a tile step: a row of 64 bytes
 
-// What a sum becomes.
-struct LinearOut {
-  float ws[4], b[4];
+// Waits until at most N of this wave's loads are under way, its LDS reads are done, and the other
+// waves have come here.
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+  static_assert(N >= 0 && N < 64, "what the counter holds");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 7 << 4);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// What the sums of N channels from n become: scales and bias.
+template <int N>
+struct Channels {
+  float s[N], b[N];
+  bool bias;
+  __device__ __forceinline__ Channels(const LinearArgs& a, int64_t n) : bias(a.bias.p != nullptr) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      s[i] = n + i < a.n ? a.w.scale[n + i] : 0.0f;
+      b[i] = bias && n + i < a.n ? load1(a.bias, n + i) : 0.0f;
+    }
+  }
+  __device__ __forceinline__ float operator()(int i, int acc, float xs) const {
+    const float v = (float)acc * xs * s[i];
+    return bias ? v + b[i] : v;
+  }
 };
-__device__ __forceinline__ void linear_store(const LinearArgs& a, int64_t m, int64_t n, const i32x4& acc, float xs,
-                                             const float (&ws)[4], const float (&b)[4]) {
-  float v[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = (float)acc[i] * xs * ws[i];
-    if (a.bias.p) v[i] += b[i];
-  }
-  store4(a.y, m, n, a.n, v);
-}
-__device__ __forceinline__ void channel4(const LinearArgs& a, int64_t n, float (&ws)[4], float (&b)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    ws[i] = n + i < a.n ? a.w.scale[n + i] : 0.0f;
-    b[i] = a.bias.p && n + i < a.n ? load1(a.bias, n + i) : 0.0f;
-  }
-}
 
-template <int BM, int BN, int WM, int WN>
-__global__ void __launch_bounds__(WM* WN * 64) linear_kernel(LinearArgs a, uint32_t tiles_m, uint32_t tiles_n, int64_t steps,
+// kStages: tile steps in LDS.
+template <int BM, int BN, int WM, int WN, int kStages>
+__global__ void __launch_bounds__(WM* WN * 64, 2) linear_kernel(LinearArgs a, uint32_t tiles_m, uint32_t tiles_n, int64_t steps,
                                                             int64_t per_split) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host's compilation has no use for it, and stumbles over the builtins
   constexpr int W = WM * WN, T = W * 64;
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16x16 results of a wave
-  constexpr int LX = BM * 8 / T, LW = BN * 8 / T;      // 16-byte loads of a thread
-  static_assert(BM * 8 % T == 0 && BN * 8 % T == 0, "whole loads");
-  __shared__ __attribute__((aligned(1024))) char lds[2][(BM + BN) * kStepK];
+  constexpr int LX = BM * 4 / T, LW = BN * 4 / T;      // 16-byte loads of a thread
+  static_assert(BM * 4 % T == 0 && BN * 4 % T == 0, "whole loads");
+  static_assert(TN == 4, "a lane's results of a row are 16 consecutive ones");
+  __shared__ __attribute__((aligned(1024))) char lds[kStages][(BM + BN) * kStepK];
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const Tile tile = tile_of(blockIdx.x, tiles_m, tiles_n);
   const int64_t m0 = tile.i * BM, n0 = tile.j * BN;
-  const int64_t first = (int64_t)blockIdx.y * per_split, last = first + per_split < steps ? first + per_split : steps;
+  const int first = (int)(blockIdx.y * per_split), last = (int)(first + per_split < steps ? first + per_split : steps);
   const int chunks = (int)((a.k + 15) >> 4);  // 16-byte chunks of a row
 
-  // A wave's load fills 8 rows of 128 bytes; chunk c of row r lies in place c ^ (r / 2 % 8), so that
-  // the sixteen rows a fragment read takes at one k lie in different banks.  Rows past the end read
-  // the last one, and their results are not stored.
+  // A wave's load fills 16 rows of 64 bytes; chunk c of row r lies in place c ^ (-r / 4 % 4): the LDS
+  // serves a 16-byte read to lanes 0-3, 12-15, 20-23 and 24-27 at a time (and to the three other such
+  // sets), whose rows and chunks then lie in different banks.  Rows past the end read the last one,
+  // and their results are not stored.
   const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(a.x.q + m0 * a.x.pitch, 0, 0xFFFFFFFFu, 0x00020000);
   const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(a.w.q + n0 * a.w.pitch, 0, 0xFFFFFFFFu, 0x00020000);
   const int mlast = (int)(a.m - 1 - m0 < BM - 1 ? a.m - 1 - m0 : BM - 1);
   const int nlast = (int)(a.n - 1 - n0 < BN - 1 ? a.n - 1 - n0 : BN - 1);
-  const auto fill = [&](int buf, int64_t step) __attribute__((always_inline)) {
-    const int c0 = (int)step * 8;
+  const int chunk = (lane & 3) ^ (-(lane >> 4) & 3);  // of this thread's loads: r / 4 % 4 is lane / 16
+  uint32_t at[LX + LW];  // of a step's loads, from the step's first byte
 #pragma unroll
-    for (int u = 0; u < LX + LW; ++u) {
-      const int r = ((u < LX ? u : u - LX) * W + wave) * 8 + (lane >> 3);
-      const int edge = u < LX ? mlast : nlast;
-      int c = c0 + ((lane & 7) ^ ((r >> 1) & 7));
-      c = c < chunks ? c : chunks - 1;
-      const uint32_t at = (uint32_t)(r < edge ? r : edge) * (uint32_t)(u < LX ? a.x.pitch : a.w.pitch) + (uint32_t)c * 16u;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(u < LX ? xr : wr, (ZS_LDS(void)*)(&lds[buf][(u * W + wave) * 1024]), 16, at, 0, 0, 0);
-    }
+  for (int u = 0; u < LX + LW; ++u) {
+    int r = ((u < LX ? u : u - LX) * W + wave) * 16 + (lane >> 2);
+    // Row 16 j + i of each 64 of w's tile holds channel 16 (i / 4) + 4 j + i % 4: a lane's results in
+    // a wave's four products j, which are rows 4 (lane / 16) + 0..3 there, are then 16 channels in a
+    // row, and two stores fill whole lines (runs of 8, and 64 bytes by each store, took 2% longer).
+    if (u >= LX) r = (r & ~63) | (r & 12) << 2 | (r & 48) >> 2 | (r & 3);
+    const int edge = u < LX ? mlast : nlast;
+    at[u] = (uint32_t)(r < edge ? r : edge) * (uint32_t)(u < LX ? a.x.pitch : a.w.pitch) + chunk * 16u;
+  }
+  const auto fill = [&](int step) __attribute__((always_inline)) {
+    // chunks past a row's end read its last one; fetch() leaves them out
+    const int most = chunks - 1 - step * 4;
+    const int back = chunk > most ? (most - chunk) * 16 : 0;
+    char* to = lds[step % kStages];
+#pragma unroll
+    for (int u = 0; u < LX + LW; ++u)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(u < LX ? xr : wr, (ZS_LDS(void)*)(to + (u * W + wave) * 1024), 16, at[u] + back,
+                                               step * kStepK, 0, 0);
   };
 
   const int wm = wave / WN, wn = wave % WN;
   const int l16 = lane & 15, l4 = lane >> 4;
-  const int xrow = (wm * TM * 16 + l16) * kStepK, wrow = (BM + wn * TN * 16 + l16) * kStepK;
+  const int place = (l4 ^ (-(l16 >> 2) & 3)) * 16;
+  const int xrow = (wm * TM * 16 + l16) * kStepK + place, wrow = (BM + wn * TN * 16 + l16) * kStepK + place;
   i32x4 acc[TM][TN] = {};
-  const auto compute = [&](int buf, int left) __attribute__((always_inline)) {  // left: chunks of the row from here on
+  i32x4 xa[TM], wa[TN], xb[TM], wb[TN];
+  const auto fetch = [&](int step, i32x4 (&xf)[TM], i32x4 (&wf)[TN]) __attribute__((always_inline)) {
+    const char* from = lds[step % kStages];
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      const int place = ((ks * 4 + l4) ^ (l16 >> 1)) * 16;
-      i32x4 xf[TM], wf[TN];
+    for (int j = 0; j < TN; ++j) wf[j] = *(const i32x4*)(from + wrow + j * 16 * kStepK);
 #pragma unroll
-      for (int i = 0; i < TM; ++i) xf[i] = *(const i32x4*)(&lds[buf][xrow + i * 16 * kStepK + place]);
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        wf[j] = *(const i32x4*)(&lds[buf][wrow + j * 16 * kStepK + place]);
-        if (left < 8 && ks * 4 + l4 >= left) wf[j] = i32x4{0, 0, 0, 0};
-      }
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[j], xf[i], acc[i][j], 0, 0, 0);
-    }
+    for (int i = 0; i < TM; ++i) xf[i] = *(const i32x4*)(from + xrow + i * 16 * kStepK);
   };
-
-  if (first < last) fill(0, first);
-  int buf = 0;
-  for (int64_t s = first; s < last; ++s) {
-    __syncthreads();  // this step's loads are done, and nobody reads the other buffer any more
-    if (s + 1 < last) fill(buf ^ 1, s + 1);
-    compute(buf, chunks - (int)s * 8);
-    buf ^= 1;
+  // Step s: its fragments are in registers and its place in LDS is free, so the step kStages ahead is
+  // requested into it; the next step's fragments are read while this one's are multiplied.
+  const auto run = [&](auto inner, int s, i32x4 (&xf)[TM], i32x4 (&wf)[TN], i32x4 (&xn)[TM], i32x4 (&wn)[TN])
+                       __attribute__((always_inline)) {
+    constexpr bool kInner = decltype(inner)::value;  // kStages steps or more follow
+    if (kInner || s + kStages - 1 < last) wait_and_meet<(kStages - 2) * (LX + LW)>();
+    else wait_and_meet<0>();
+    if (kInner || s + kStages < last) fill(s + kStages);
+    if (kInner || s + 1 < last) fetch(s + 1, xn, wn);
+    if (!kInner && chunks - s * 4 < 4) {  // the end of the rows
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        if (l4 >= chunks - s * 4) wf[j] = i32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[j], xf[i], acc[i][j], 0, 0, 0);
+  };
+  if (first < last) {
+#pragma unroll
+    for (int k = 0; k < kStages; ++k)
+      if (first + k < last) fill(first + k);
+    wait_and_meet<0>();
+    fetch(first, xa, wa);
+    int s = first;
+    for (; s + 1 + kStages < last; s += 2) {
+      run(std::true_type(), s, xa, wa, xb, wb);
+      run(std::true_type(), s + 1, xb, wb, xa, wa);
+    }
+    for (; s < last; s += 2) {
+      run(std::false_type(), s, xa, wa, xb, wb);
+      if (s + 1 < last) run(std::false_type(), s + 1, xb, wb, xa, wa);
+    }
   }
 
-  // results: row n0 + 4 (lane / 16) + element, column m0 + lane % 16 of each 16x16
-#pragma unroll
-  for (int j = 0; j < TN; ++j) {
-    const int64_t n = n0 + wn * TN * 16 + j * 16 + l4 * 4;
-    float ws[4], b[4];
-    if (n >= a.n) continue;
-    if (!a.part) channel4(a, n, ws, b);
+  // a lane has, of row m0 + lane % 16 of each 16, the channels n to n + 15
+  const int64_t n = n0 + wn * 64 + l4 * 16;
+  if (n >= a.n) return;
+  if (a.part) {
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       const int64_t m = m0 + wm * TM * 16 + i * 16 + l16;
       if (m >= a.m) continue;
-      if (a.part) *(i32x4*)(a.part + ((int64_t)blockIdx.y * a.m + m) * a.n4 + n) = acc[i][j];
-      else linear_store(a, m, n, acc[i][j], a.x.scale[m], ws, b);
+      int32_t* to = a.part + ((int64_t)blockIdx.y * a.m + m) * a.n4 + n;
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        if (n + 4 * j < a.n) *(i32x4*)(to + 4 * j) = acc[i][j];
     }
+    return;
   }
+  const Channels<16> ch(a, n);
+  with_type(a.y.dtype, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int64_t m = m0 + wm * TM * 16 + i * 16 + l16;
+      if (m >= a.m) continue;
+      const float xs = a.x.scale[m];
+      float v[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v[k] = ch(k, acc[i][k >> 2][k & 3], xs);
+      store_run<DT, 16>((char*)a.y.p + m * a.y.pitch * esize(DT), n, a.n, v);
+    }
+  });
+#endif
 }
 
 // Adds the splits' integer sums, which no order changes.
@@ -184,9 +276,15 @@ __global__ void __launch_bounds__(256) linear_join_kernel(LinearArgs a, int spli
     const int64_t m = q / quads, n = q % quads * 4;
     i32x4 acc = {0, 0, 0, 0};
     for (int s = 0; s < splits; ++s) acc += *(const i32x4*)(a.part + ((int64_t)s * a.m + m) * a.n4 + n);
-    float ws[4], b[4];
-    channel4(a, n, ws, b);
-    linear_store(a, m, n, acc, a.x.scale[m], ws, b);
+    const Channels<4> ch(a, n);
+    const float xs = a.x.scale[m];
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = ch(k, acc[k], xs);
+    with_type(a.y.dtype, [&](auto dt) {
+      constexpr int DT = decltype(dt)::value;
+      store_run<DT, 4>((char*)a.y.p + m * a.y.pitch * esize(DT), n, a.n, v);
+    });
   }
 }
 
@@ -373,13 +471,7 @@ __global__ void __launch_bounds__(WI* WJ * 64) grad_kernel(GradArgs g, uint32_t 
         continue;
       }
       float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-      if (g.accumulate) {
-        float old[4];
-        load4(g.c, r, c, g.nj, old);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] += old[k];
-      }
-      store4(g.c, r, c, g.nj, v);
+      with_type(g.c.dtype, [&](auto dt) { finish_run<decltype(dt)::value, 4>(g.c, r, c, g.nj, g.accumulate, v); });
     }
   }
 }
@@ -392,13 +484,7 @@ __global__ void __launch_bounds__(256) grad_join_kernel(GradArgs g, int splits) 
     f32x4 acc = {0, 0, 0, 0};
     for (int s = 0; s < splits; ++s) acc += *(const f32x4*)(g.part + ((int64_t)s * g.ni + r) * g.nj4 + c);
     float v[4] = {acc[0], acc[1], acc[2], acc[3]};
-    if (g.accumulate) {
-      float old[4];
-      load4(g.c, r, c, g.nj, old);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] += old[k];
-    }
-    store4(g.c, r, c, g.nj, v);
+    with_type(g.c.dtype, [&](auto dt) { finish_run<decltype(dt)::value, 4>(g.c, r, c, g.nj, g.accumulate, v); });
   }
 }
 
@@ -450,6 +536,7 @@ static int64_t join_grid(int64_t quads) {
 // block each, but no finer than four steps to a split.
 static ProductPlan plan_product(int64_t ni, int64_t nj, int64_t steps, int64_t bi, int64_t bj, int64_t elem) {
   ProductPlan p{};
+  p.tile = (int32_t)bi;
   p.tiles_i = up(ni, bi);
   p.tiles_j = up(nj, bj);
   p.steps = steps;
@@ -462,11 +549,15 @@ static ProductPlan plan_product(int64_t ni, int64_t nj, int64_t steps, int64_t b
   return p;
 }
 
-ProductPlan plan_linear(int64_t m, int64_t k, int64_t n) { return plan_product(m, n, up(k, kStepK), 128, 128, 4); }
+ProductPlan plan_linear(int64_t m, int64_t k, int64_t n) {
+  const ProductPlan p = plan_product(m, n, up(k, kStepK), 256, 256, 4);
+  return p.tiles_i * p.tiles_j >= 256 ? p : plan_product(m, n, up(k, kStepK), 128, 128, 4);
+}
 
 hipError_t launch_linear(const LinearArgs& a, const ProductPlan& p, hipStream_t st) {
   const dim3 grid((uint32_t)(p.tiles_i * p.tiles_j), (uint32_t)p.splits);
-  linear_kernel<128, 128, 2, 2><<<grid, 256, 0, st>>>(a, (uint32_t)p.tiles_i, (uint32_t)p.tiles_j, p.steps, up(p.steps, p.splits));
+  if (p.tile == 256) linear_kernel<256, 256, 2, 4, 4><<<grid, 512, 0, st>>>(a, (uint32_t)p.tiles_i, (uint32_t)p.tiles_j, p.steps, up(p.steps, p.splits));
+  else linear_kernel<128, 128, 2, 2, 4><<<grid, 256, 0, st>>>(a, (uint32_t)p.tiles_i, (uint32_t)p.tiles_j, p.steps, up(p.steps, p.splits));
   if (a.part) linear_join_kernel<<<(uint32_t)join_grid(a.m * a.n4 / 4), 256, 0, st>>>(a, (int)p.splits);
   return hipGetLastError();
 }
