@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) linear_kernel(LinearArgs a, ui
     // chunks past a row's end read its last one; fetch() leaves them out
     const int most = chunks - 1 - step * 4;
     const int back = chunk > most ? (most - chunk) * 16 : 0;
-    char* to = lds[step % kStages];
+    char* to = lds[(unsigned)step % kStages];
 #pragma unroll
     for (int u = 0; u < LX + LW; ++u)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(u < LX ? xr : wr, (ZS_LDS(void)*)(to + (u * W + wave) * 1024), 16, at[u] + back,
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) linear_kernel(LinearArgs a, ui
   i32x4 acc[TM][TN] = {};
   i32x4 xa[TM], wa[TN], xb[TM], wb[TN];
   const auto fetch = [&](int step, i32x4 (&xf)[TM], i32x4 (&wf)[TN]) __attribute__((always_inline)) {
-    const char* from = lds[step % kStages];
+    const char* from = lds[(unsigned)step % kStages];
 #pragma unroll
     for (int j = 0; j < TN; ++j) wf[j] = *(const i32x4*)(from + wrow + j * 16 * kStepK);
 #pragma unroll
@@ -293,13 +293,21 @@ __global__ void __launch_bounds__(256) linear_join_kernel(LinearArgs a, int spli
 // instructions.  Tiles lie in LDS as [s][..] (or [i][s]); the instruction wants each lane's
 // values along s, which the transposing LDS read gives.
 
-constexpr int kStepC = 64;
+constexpr int kStepS = 32;  // s of a tile step: one matrix instruction's
 
-// Place of 16-element segment g of row s in a tile [s][...]: the rows that a transposing read takes
-// together lie in different banks.
+// How a comes into LDS.
+enum Feed : int {
+  kDirect = 0,  // bf16 as it is, loaded into LDS: rows and columns on 16-byte boundaries
+  kPlain = 1,   // bf16 as it is, through registers, at any alignment
+  kScaled = 2,  // times the scales, as two bf16 terms, through registers
+};
+
+// Place of 16-element segment g of row s in a tile [s][...] is g ^ this: the rows that a transposing
+// read takes together lie in different banks.
 __device__ __forceinline__ int seg_swizzle(int s) { return (s & 3) | ((s >> 1) & 4); }
 
-// Splits v into two bf16 values whose sum is v to 16 bits (exactly, if it has no more).
+// Splits two values into two bf16 values each whose sum is theirs to 16 bits (exactly, if they have
+// no more).
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
   hi = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
   const float ha = dec_lo<ZERO_BF16>(hi), hb = dec_hi<ZERO_BF16>(hi);
@@ -308,172 +316,306 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   lo = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{ra, rb}), bf16x2));
 }
 
-// TWO: the scales go into a, whose values then take two bf16 terms; else into q's, exactly.
-template <int DT, bool TRANS, bool TWO, int BI, int BJ, int WI, int WJ>
-__global__ void __launch_bounds__(WI* WJ * 64) grad_kernel(GradArgs g, uint32_t tiles_i, uint32_t tiles_j, int64_t steps,
-                                                          int64_t per_split) {
-  constexpr int T = WI * WJ * 64, S = kStepC;
+template <int DT, bool TRANS, int FEED, int BI, int BJ, int WI, int WJ>
+__global__ void __launch_bounds__(WI* WJ * 64, 2) grad_kernel(GradArgs g, uint32_t tiles_i, uint32_t tiles_j, int64_t steps,
+                                                             int64_t per_split) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host's compilation has no use for it, and stumbles over the builtins
+  constexpr int W = WI * WJ, T = W * 64, S = kStepS;
   constexpr int TI = BI / WI / 16, TJ = BJ / WJ / 16;
-  constexpr int LA = BI * S / 8 / T, LQ = BJ * S / 16 / T;  // chunks of a thread
-  constexpr int ABYTES = BI * S * 2, TERMS = TWO ? 2 : 1;
+  constexpr int LA = BI * S / 8 / T, LQ = BJ * S / 16 / T;  // 16-byte chunks of a thread
+  constexpr int TERMS = FEED == kScaled ? 2 : 1;
+  constexpr int ABYTES = BI * S * 2, STEP = ABYTES * TERMS + BJ * S * 2;
+  constexpr int kStages = FEED == kDirect ? 4 : 3;  // tile steps in LDS
   static_assert(BI * S / 8 % T == 0 && BJ * S / 16 % T == 0, "whole chunks");
-  __shared__ __attribute__((aligned(1024))) char lds[2][ABYTES * TERMS + BJ * S * 2];
+  static_assert(TJ == 4, "a lane's results of a row are 16 consecutive ones");
+  __shared__ __attribute__((aligned(1024))) char lds[kStages][STEP];
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const Tile tile = tile_of(blockIdx.x, tiles_i, tiles_j);
   const int64_t i0 = tile.i * BI, j0 = tile.j * BJ;
-  const int64_t first = (int64_t)blockIdx.y * per_split, last = first + per_split < steps ? first + per_split : steps;
+  const int first = (int)(blockIdx.y * per_split), last = (int)(first + per_split < steps ? first + per_split : steps);
 
-  Raw8<ZERO_BF16> ra[LA];
-  u32x4 rq[LQ];
-  float rs[TWO ? (TRANS ? LA : 1) : LQ];
-  float rs8[TWO && !TRANS ? LA : 1][8];
-  const auto fetch = [&](int64_t step) __attribute__((always_inline)) {
-    const int64_t s0 = step * S;
+  // --- a, loaded into LDS: a wave's load fills 1024 bytes in the order of the lanes
+  uint32_t at[LA];  // from the step's first element
+  if constexpr (FEED == kDirect) {
 #pragma unroll
     for (int u = 0; u < LA; ++u) {
-      const int id = u * T + t;
-      if constexpr (TRANS) {
-        const int64_t s = s0 + id / (BI / 8), i = i0 + id % (BI / 8) * 8;
-        const bool in = s < g.nc;
-        ra[u] = load8<ZERO_BF16>((const char*)g.a.p + (in ? s : 0) * g.a.pitch * 2, i, in ? g.ni : 0);
-        if constexpr (TWO) rs[u] = in ? g.q.scale[s] : 0.0f;
-      } else {
-        const int64_t i = i0 + id / (S / 8), s = s0 + id % (S / 8) * 8;
-        const bool in = i < g.ni;
-        ra[u] = load8<ZERO_BF16>((const char*)g.a.p + (in ? i : 0) * g.a.pitch * 2, s, in ? g.nc : 0);
-        if constexpr (TWO) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) rs8[u][k] = s + k < g.nc ? g.q.scale[s + k] : 0.0f;
-        }
+      const int id = (u * W + wave) * 64 + lane;
+      if constexpr (TRANS) {  // columns past the end read the last ones, and their results are not stored
+        const int s = id / (BI / 8), c = id % (BI / 8) ^ (seg_swizzle(s) << 1);
+        const int64_t i = i0 + c * 8 < g.ni ? c * 8 : g.ni - 8 - i0;
+        at[u] = (uint32_t)s * (uint32_t)(g.a.pitch * 2) + (uint32_t)(i * 2);
+      } else {  // rows likewise; the chunks' order is that of the linear layer's tiles
+        const int i = id / 4, c = id % 4 ^ (-(i >> 2) & 3);
+        at[u] = (uint32_t)(i0 + i < g.ni ? i : g.ni - 1 - i0) * (uint32_t)(g.a.pitch * 2) + c * 16u;
       }
     }
-#pragma unroll
-    for (int u = 0; u < LQ; ++u) {
-      const int id = u * T + t;
-      const int64_t s = s0 + id / (BJ / 16), j = j0 + id % (BJ / 16) * 16;
-      const bool in = s < g.nc && j < g.nj;
-      rq[u] = in ? *(const u32x4*)(g.q.q + s * g.q.pitch + j) : u32x4{0, 0, 0, 0};
-      if constexpr (!TWO) rs[u] = in ? g.q.scale[s] : 0.0f;
-    }
-  };
-  const auto stage = [&](int buf) __attribute__((always_inline)) {
-    char* la = lds[buf];
-    char* lq = lds[buf] + ABYTES * TERMS;
+  }
+  const auto fill = [&](auto inner, int step) __attribute__((always_inline)) {
+    const int64_t s0 = (int64_t)step * S;
+    const char* base = (const char*)g.a.p + (TRANS ? s0 * g.a.pitch + i0 : i0 * g.a.pitch + s0) * 2;
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, 0xFFFFFFFFu, 0x00020000);
+    // past the end of s the last row or chunk is read; multiply() leaves it out
+    const int over = (int)(s0 + S - g.nc);
+    char* to = lds[(unsigned)step % kStages];
 #pragma unroll
     for (int u = 0; u < LA; ++u) {
-      const int id = u * T + t;
-      int at;
-      if constexpr (TRANS) {
-        const int s = id / (BI / 8), c = id % (BI / 8);
-        at = s * BI * 2 + (((c >> 1) ^ seg_swizzle(s)) << 5) + (c & 1) * 16;
-      } else {
-        const int i = id / (S / 8), c = id % (S / 8);
-        at = i * S * 2 + ((c ^ ((i >> 1) & 7)) << 4);
-      }
-      if constexpr (TWO) {
-        u32x4 hi, lo;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float s0 = TRANS ? rs[TRANS ? u : 0] : rs8[TRANS ? 0 : u][2 * k], s1 = TRANS ? rs[TRANS ? u : 0] : rs8[TRANS ? 0 : u][2 * k + 1];
-          uint32_t h, l;
-          split2(dec_lo<DT>(ra[u].v[0][k]) * s0, dec_hi<DT>(ra[u].v[0][k]) * s1, h, l);
-          hi[k] = h;
-          lo[k] = l;
+      uint32_t o = at[u];
+      if (!decltype(inner)::value && over > 0) {
+        const int id = (u * W + wave) * 64 + lane;
+        if constexpr (TRANS) {
+          const int s = id / (BI / 8), end = S - 1 - over;
+          if (s > end) o -= (uint32_t)(s - end) * (uint32_t)(g.a.pitch * 2);
+        } else {
+          const int i = id / 4, c = id % 4 ^ (-(i >> 2) & 3), end = (S - over) / 8 - 1;
+          if (c > end) o -= (uint32_t)(c - end) * 16u;
         }
-        *(u32x4*)(la + at) = hi;
-        *(u32x4*)(la + ABYTES + at) = lo;
-      } else {
-        *(u32x4*)(la + at) = ra[u].v[0];
       }
-    }
-#pragma unroll
-    for (int u = 0; u < LQ; ++u) {
-      const int id = u * T + t;
-      const int s = id / (BJ / 16), c = id % (BJ / 16);
-      char* to = lq + s * BJ * 2 + ((c ^ seg_swizzle(s)) << 5);
-      const float scale = TWO ? 1.0f : rs[TWO ? 0 : u];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        u32x4 o;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t w = rq[u][2 * h + (k >> 1)];
-          const f32x2 v = {q_of(w, (k & 1) * 2) * scale, q_of(w, (k & 1) * 2 + 1) * scale};
-          o[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
-        }
-        *(u32x4*)(to + 16 * h) = o;
-      }
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (ZS_LDS(void)*)(to + (u * W + wave) * 1024), 16, o, 0, 0, 0);
     }
   };
 
+  // --- through registers: two steps' worth, loaded two steps before they are written to LDS
+  struct Held {
+    Raw8<ZERO_BF16> a[FEED == kDirect ? 1 : LA];
+    float as[FEED == kScaled ? (TRANS ? LA : LA * 8) : 1];
+    u32x4 q[LQ];
+    float qs[LQ];
+  } held[2];
+  // Row and segment of 16 columns of a thread's chunks of q: four lanes take 64 columns, the next ones
+  // the same of the three following rows, which they write to different banks.
+  const auto q_row = [&](int u) __attribute__((always_inline)) { return (u * T + t) / (BJ / 4) * 4 + (t >> 2 & 3); };
+  const auto q_seg = [&](int u) __attribute__((always_inline)) { return (u * T + t) % (BJ / 4) / 16 * 4 + (t & 3); };
+  uint32_t qat[LQ];  // of the chunks, from the step's first byte; columns past the end read the first ones
+#pragma unroll
+  for (int u = 0; u < LQ; ++u) {
+    const int c = q_seg(u) * 16;
+    qat[u] = (uint32_t)q_row(u) * (uint32_t)g.q.pitch + (j0 + c < g.nj ? (uint32_t)c : 0u);
+  }
+  const bool whole = TRANS ? i0 + BI <= g.ni : i0 + BI <= g.ni && g.nc >= S;  // the tile's rows or columns of a
+  const auto load = [&](auto inner, int step, Held& h) __attribute__((always_inline)) {
+    constexpr bool kInner = decltype(inner)::value;  // not the last step
+    const int64_t s0 = (int64_t)step * S;
+    const int left = kInner || g.nc - s0 > S ? S : (int)(g.nc - s0);
+    if constexpr (FEED != kDirect) {
+      const char* base = (const char*)g.a.p + (TRANS ? s0 * g.a.pitch + i0 : i0 * g.a.pitch + s0) * 2;
+      const int64_t cols = TRANS ? g.ni - i0 : left;
+#pragma unroll
+      for (int u = 0; u < LA; ++u) {
+        const int id = u * T + t;
+        const int r = TRANS ? id / (BI / 8) : id / (S / 8), c = (TRANS ? id % (BI / 8) : id % (S / 8)) * 8;
+        const char* row = base + (int64_t)r * g.a.pitch * 2;
+        if (whole && (kInner || left == S)) {
+          h.a[u] = load_any<Raw8<ZERO_BF16>>(row + c * 2);
+        } else {
+          const bool in = TRANS ? r < left : i0 + r < g.ni;
+          h.a[u] = load8<ZERO_BF16>(in ? row : base, c, in ? cols : 0);
+        }
+        if constexpr (FEED == kScaled) {
+          if constexpr (TRANS) {
+            h.as[u] = g.q.scale[s0 + (r < left ? r : left - 1)];
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) h.as[u * 8 + k] = g.q.scale[s0 + (c + k < left ? c + k : left - 1)];
+          }
+        }
+      }
+    }
+    const char* base = (const char*)g.q.q + s0 * g.q.pitch + j0;
+    const float* scale = g.q.scale + s0;
+#pragma unroll
+    for (int u = 0; u < LQ; ++u) {
+      const int r = q_row(u);
+      if (kInner) {
+        h.q[u] = *(const u32x4*)(base + qat[u]);
+        if constexpr (FEED != kScaled) h.qs[u] = scale[r];
+      } else {  // rows past the end read the last one, and count nothing
+        const int back = r < left ? 0 : r - left + 1;
+        h.q[u] = *(const u32x4*)(base + (qat[u] - (uint32_t)back * (uint32_t)g.q.pitch));
+        if (back) h.q[u] = u32x4{0, 0, 0, 0};
+        if constexpr (FEED != kScaled) h.qs[u] = back ? 0.0f : scale[r];
+      }
+    }
+  };
+  const auto stage = [&](int step, Held& h) __attribute__((always_inline)) {
+    char* la = lds[(unsigned)step % kStages];
+    char* lq = la + ABYTES * TERMS;
+    if constexpr (FEED != kDirect) {
+#pragma unroll
+      for (int u = 0; u < LA; ++u) {
+        const int id = u * T + t;
+        int to;
+        if constexpr (TRANS) {
+          const int s = id / (BI / 8), c = id % (BI / 8);
+          to = s * BI * 2 + ((c ^ (seg_swizzle(s) << 1)) << 4);
+        } else {
+          const int i = id / (S / 8), c = id % (S / 8);
+          to = i * S * 2 + ((c ^ (-(i >> 2) & 3)) << 4);
+        }
+        if constexpr (FEED == kScaled) {
+          u32x4 hi, lo;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float s0 = h.as[TRANS ? u : u * 8 + 2 * k], s1 = h.as[TRANS ? u : u * 8 + 2 * k + 1];
+            uint32_t x, y;
+            split2(dec_lo<DT>(h.a[u].v[0][k]) * s0, dec_hi<DT>(h.a[u].v[0][k]) * s1, x, y);
+            hi[k] = x;
+            lo[k] = y;
+          }
+          *(u32x4*)(la + to) = hi;
+          *(u32x4*)(la + ABYTES + to) = lo;
+        } else {
+          *(u32x4*)(la + to) = h.a[u].v[0];
+        }
+      }
+    }
+    // Quads k of a segment of 16 columns go to the four segments of its 64: position 16 k + 4 c + e holds
+    // column 16 c + 4 k + e, so that a lane's results, rows 4 (lane / 16) + 0..3 of a wave's four
+    // products, are 16 columns in a row.
+#pragma unroll
+    for (int u = 0; u < LQ; ++u) {
+      const int s = q_row(u), c = q_seg(u);
+      // as unsigned bytes q + 128, which take one instruction each: (q + 128) scale - 128 scale, exact
+      const float scale = FEED == kScaled ? 1.0f : h.qs[u], shift = -128.0f * scale;
+      asm volatile("" : "+v"(h.q[u]));  // not taken apart before: its bytes in a register each would wait for it
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        u32x2 o;
+        const uint32_t w = h.q[u][k] ^ 0x80808080u;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const f32x2 v = {__builtin_fmaf((float)(uint8_t)(w >> (16 * e)), scale, shift),
+                           __builtin_fmaf((float)(uint8_t)(w >> (16 * e + 8)), scale, shift)};
+          o[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+        }
+        *(u32x2*)(lq + s * BJ * 2 + ((((c & ~3) + k) ^ seg_swizzle(s)) << 5) + (c & 3) * 8) = o;
+      }
+    }
+  };
+
+  // --- products
   const int wi = wave / WJ, wj = wave % WJ;
   const int l16 = lane & 15, l4 = lane >> 4;
   // a transposing read takes, in each sixteen lanes, four rows of sixteen columns
   const int trow = l4 * 8 + (l16 >> 2), tcol = (l16 & 3) * 8, tswz = seg_swizzle(trow);
   f32x4 acc[TI][TJ] = {};
-  const auto frag_t = [&](const char* base, int width, int seg, int ks) __attribute__((always_inline)) {
-    const char* p = base + trow * width * 2 + ((seg ^ tswz) << 5) + tcol + ks * 32 * width * 2;
+  bf16x8 fa[TERMS][TI], fq[TJ];
+  const auto frag_t = [&](const char* base, int width, int seg) __attribute__((always_inline)) {
+    const char* p = base + trow * width * 2 + ((seg ^ tswz) << 5) + tcol;
     const bf16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((ZS_LDS(bf16x4)*)p);
     const bf16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((ZS_LDS(bf16x4)*)(p + 4 * width * 2));
     return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
   };
-  const auto compute = [&](int buf) __attribute__((always_inline)) {
-    const char* la = lds[buf];
-    const char* lq = lds[buf] + ABYTES * TERMS;
-#pragma unroll
-    for (int ks = 0; ks < S / 32; ++ks) {
-      bf16x8 qf[TJ];
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) qf[j] = frag_t(lq, BJ, wj * TJ + j, ks);
-#pragma unroll
-      for (int h = 0; h < TERMS; ++h) {
-        bf16x8 af[TI];
+  const auto fetch_q = [&](int step, int j) __attribute__((always_inline)) {
+    return frag_t(lds[(unsigned)step % kStages] + ABYTES * TERMS, BJ, wj * TJ + j);
+  };
+  const auto fetch_a = [&](int step, int h, int i) __attribute__((always_inline)) {
+    const char* la = lds[(unsigned)step % kStages] + h * ABYTES;
+    if constexpr (TRANS) return frag_t(la, BI, wi * TI + i);
+    else return *(const bf16x8*)(la + ((wi * TI + i) * 16 + l16) * S * 2 + ((l4 ^ (-(l16 >> 2) & 3)) << 4));
+  };
+  // Step s: its fragments of a and the first two of q are in registers; the last two are read while the
+  // first are multiplied, then the next step's into the registers that the products are done with.
+  // The step before has left its place in LDS to the step three ahead (a, loaded into it); the step
+  // two ahead is converted into its place, and the one four ahead requested into the
+  // registers that it leaves.
+  const auto run = [&](auto inner, int s, Held& h) __attribute__((always_inline)) {
+    constexpr bool kInner = decltype(inner)::value;  // five steps or more follow
+    constexpr int kLoads = LA + 2 * LQ;              // of a step, where a is loaded into LDS
+    const bool more = kInner || s + 1 < last;
+    if constexpr (FEED == kDirect) {
+      if (kInner || s + 2 < last) wait_and_meet<kLoads + 2 * LQ>();
+      else wait_and_meet<0>();
+      if (kInner || s + 3 < last) fill(inner, s + 3);
+    } else {
+      wait_and_meet<63>();
+    }
+    fq[2] = fetch_q(s, 2);
+    fq[3] = fetch_q(s, 3);
+    if (kInner || s + 2 < last) stage(s + 2, h);
+    if (kInner || s + 4 < last) load(inner, s + 4, h);
+    if constexpr (FEED == kDirect) {
+      if (!kInner && (int64_t)(s + 1) * S > g.nc) {  // rows of s past the end
+        const int left = (int)(g.nc - (int64_t)s * S) - l4 * 8;
 #pragma unroll
         for (int i = 0; i < TI; ++i) {
-          if constexpr (TRANS) {
-            af[i] = frag_t(la + h * ABYTES, BI, wi * TI + i, ks);
-          } else {
-            const int row = (wi * TI + i) * 16 + l16;
-            af[i] = *(const bf16x8*)(la + h * ABYTES + row * S * 2 + (((ks * 4 + l4) ^ (l16 >> 1)) << 4));
-          }
+          u32x4 w = __builtin_bit_cast(u32x4, fa[0][i]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] &= left >= 2 * k + 2 ? 0xFFFFFFFFu : left == 2 * k + 1 ? 0xFFFFu : 0u;
+          fa[0][i] = __builtin_bit_cast(bf16x8, w);
         }
+      }
+    }
 #pragma unroll
-        for (int i = 0; i < TI; ++i)
+    for (int half = 0; half < 2; ++half) {
 #pragma unroll
-          for (int j = 0; j < TJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf[j], af[i], acc[i][j], 0, 0, 0);
+      for (int h2 = 0; h2 < TERMS; ++h2)
+#pragma unroll
+        for (int i = 0; i < TI; ++i) {
+#pragma unroll
+          for (int j = 2 * half; j < 2 * half + 2; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[j], fa[h2][i], acc[i][j], 0, 0, 0);
+          if (half == 1 && more) fa[h2][i] = fetch_a(s + 1, h2, i);
+        }
+      if (half == 0 && more) {
+        fq[0] = fetch_q(s + 1, 0);
+        fq[1] = fetch_q(s + 1, 1);
       }
     }
   };
-
   if (first < last) {
-    fetch(first);
-    stage(0);
-  }
-  int buf = 0;
-  for (int64_t s = first; s < last; ++s) {
-    __syncthreads();
-    if (s + 1 < last) fetch(s + 1);
-    compute(buf);
-    if (s + 1 < last) stage(buf ^ 1);
-    buf ^= 1;
-  }
-
+    if constexpr (FEED == kDirect) {
 #pragma unroll
-  for (int i = 0; i < TI; ++i) {
-    const int64_t r = i0 + (wi * TI + i) * 16 + l16;
-    if (r >= g.ni) continue;
+      for (int k = 0; k < 3; ++k)
+        if (first + k < last) fill(std::false_type(), first + k);
+    }
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) {
-      const int64_t c = j0 + (wj * TJ + j) * 16 + l4 * 4;
-      if (c >= g.nj) continue;
-      if (g.part) {
-        *(f32x4*)(g.part + ((int64_t)blockIdx.y * g.ni + r) * g.nj4 + c) = acc[i][j];
-        continue;
-      }
-      float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-      with_type(g.c.dtype, [&](auto dt) { finish_run<decltype(dt)::value, 4>(g.c, r, c, g.nj, g.accumulate, v); });
+    for (int k = 0; k < 2; ++k)
+      if (first + k < last) load(std::false_type(), first + k, held[k]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (first + k < last) stage(first + k, held[k]);
+      if (first + 2 + k < last) load(std::false_type(), first + 2 + k, held[k]);
+    }
+    wait_and_meet<0>();
+    fq[0] = fetch_q(first, 0);
+    fq[1] = fetch_q(first, 1);
+#pragma unroll
+    for (int h = 0; h < TERMS; ++h)
+#pragma unroll
+      for (int i = 0; i < TI; ++i) fa[h][i] = fetch_a(first, h, i);
+    int s = first;
+    for (; s + 6 < last; s += 2) {
+      run(std::true_type(), s, held[0]);
+      run(std::true_type(), s + 1, held[1]);
+    }
+    for (; s < last; s += 2) {
+      run(std::false_type(), s, held[0]);
+      if (s + 1 < last) run(std::false_type(), s + 1, held[1]);
     }
   }
+
+  // a lane has, of row lane % 16 of each 16, the columns c to c + 15
+  const int64_t c = j0 + wj * 64 + l4 * 16;
+  if (c >= g.nj) return;
+  with_type(g.c.dtype, [&](auto dt) {
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const int64_t r = i0 + (wi * TI + i) * 16 + l16;
+      if (r >= g.ni) continue;
+      if (g.part) {
+        float* to = g.part + ((int64_t)blockIdx.y * g.ni + r) * g.nj4 + c;
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+          if (c + 4 * j < g.nj) *(f32x4*)(to + 4 * j) = acc[i][j];
+        continue;
+      }
+      float v[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v[k] = acc[i][k >> 2][k & 3];
+      finish_run<decltype(dt)::value, 16>(g.c, r, c, g.nj, g.accumulate, v);
+    }
+  });
+#endif
 }
 
 // Adds the splits' sums, in their order.
@@ -562,21 +704,41 @@ hipError_t launch_linear(const LinearArgs& a, const ProductPlan& p, hipStream_t 
   return hipGetLastError();
 }
 
-ProductPlan plan_grad(int64_t ni, int64_t nj, int64_t nc) { return plan_product(ni, nj, up(nc, kStepC), 128, 128, 4); }
+// a goes straight into LDS if its 16-byte chunks are whole and on their boundaries; 256 rows lie within
+// 32-bit offsets.
+static bool direct(const GradArgs& g, bool trans) {
+  const int64_t along = trans ? g.ni : g.nc;
+  return g.a.dtype == ZERO_BF16 && g.q.rule == ZERO_SCALE_POW2 && (uintptr_t)g.a.p % 16 == 0 && g.a.pitch % 8 == 0 &&
+         along % 8 == 0 && along > 0 && g.a.pitch <= (int64_t)1 << 22;
+}
+ProductPlan plan_grad(int64_t ni, int64_t nj, int64_t nc) {
+  const ProductPlan p = plan_product(ni, nj, up(nc, kStepS), 256, 256, 4);
+  return p.tiles_i * p.tiles_j >= 128 ? p : plan_product(ni, nj, up(nc, kStepS), 128, 128, 4);
+}
 
-template <int DT, bool TRANS, bool TWO>
+template <int DT, bool TRANS, int FEED>
 static void launch_grad_typed(const GradArgs& g, const ProductPlan& p, hipStream_t st) {
   const dim3 grid((uint32_t)(p.tiles_i * p.tiles_j), (uint32_t)p.splits);
-  grad_kernel<DT, TRANS, TWO, 128, 128, 2, 2><<<grid, 256, 0, st>>>(g, (uint32_t)p.tiles_i, (uint32_t)p.tiles_j, p.steps, up(p.steps, p.splits));
+  const uint32_t ti = (uint32_t)p.tiles_i, tj = (uint32_t)p.tiles_j;
+  if (p.tile != 256) {
+    grad_kernel<DT, TRANS, FEED, 128, 128, 2, 2><<<grid, 256, 0, st>>>(g, ti, tj, p.steps, up(p.steps, p.splits));
+  } else if constexpr (FEED != kDirect) {  // 128 rows, whose values also lie in registers on their way
+    const uint32_t t2 = (uint32_t)up(g.ni, 128);
+    grad_kernel<DT, TRANS, FEED, 128, 256, 2, 4><<<dim3(t2 * tj, grid.y), 512, 0, st>>>(g, t2, tj, p.steps, up(p.steps, p.splits));
+  } else {
+    grad_kernel<DT, TRANS, FEED, 256, 256, 2, 4><<<grid, 512, 0, st>>>(g, ti, tj, p.steps, up(p.steps, p.splits));
+  }
 }
 
 hipError_t launch_grad(const GradArgs& g, bool trans, const ProductPlan& p, hipStream_t st) {
-  const bool two = g.a.dtype != ZERO_BF16 || g.q.rule != ZERO_SCALE_POW2;
-  if (g.a.dtype == ZERO_BF16) {
-    if (two) trans ? launch_grad_typed<ZERO_BF16, true, true>(g, p, st) : launch_grad_typed<ZERO_BF16, false, true>(g, p, st);
-    else trans ? launch_grad_typed<ZERO_BF16, true, false>(g, p, st) : launch_grad_typed<ZERO_BF16, false, false>(g, p, st);
+  if (g.a.dtype == ZERO_F16) {
+    trans ? launch_grad_typed<ZERO_F16, true, kScaled>(g, p, st) : launch_grad_typed<ZERO_F16, false, kScaled>(g, p, st);
+  } else if (g.q.rule != ZERO_SCALE_POW2) {
+    trans ? launch_grad_typed<ZERO_BF16, true, kScaled>(g, p, st) : launch_grad_typed<ZERO_BF16, false, kScaled>(g, p, st);
+  } else if (direct(g, trans)) {
+    trans ? launch_grad_typed<ZERO_BF16, true, kDirect>(g, p, st) : launch_grad_typed<ZERO_BF16, false, kDirect>(g, p, st);
   } else {
-    trans ? launch_grad_typed<ZERO_F16, true, true>(g, p, st) : launch_grad_typed<ZERO_F16, false, true>(g, p, st);
+    trans ? launch_grad_typed<ZERO_BF16, true, kPlain>(g, p, st) : launch_grad_typed<ZERO_BF16, false, kPlain>(g, p, st);
   }
   if (g.part) grad_join_kernel<<<(uint32_t)join_grid(g.ni * g.nj4 / 4), 256, 0, st>>>(g, (int)p.splits);
   return hipGetLastError();
