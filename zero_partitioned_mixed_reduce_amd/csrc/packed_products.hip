@@ -111,15 +111,27 @@ __device__ __forceinline__ void finish_run(const MatArg& c, int64_t r, int64_t c
 
 constexpr int kStepK = 64;  // k of a tile step: a row of 64 bytes
 
-// Waits until at most N of this wave's loads are under way, its LDS reads are done, and the other
-// waves have come here.
+// A tile step of a wave has two phases: it reads its fragments from LDS and prepares later steps, and it
+// multiplies.  In a block of eight waves, two to a SIMD, the second four are a phase behind, so
+// that of a SIMD's waves one multiplies while the other reads and converts (all eight in step
+// leave the matrix cores idle half of the time).  A phase ends for all waves of the block at once.
+//
+// Ends the first phase: at most N of the wave's loads are under way, all its LDS accesses done.
 template <int N>
-__device__ __forceinline__ void wait_and_meet() {
+__device__ __forceinline__ void end_reading() {
   static_assert(N >= 0 && N < 64, "what the counter holds");
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 7 << 4);
   __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
   asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ void meet() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 // What the sums of N channels from n become: scales and bias.
@@ -193,49 +205,42 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) linear_kernel(LinearArgs a, ui
   const int place = (l4 ^ (-(l16 >> 2) & 3)) * 16;
   const int xrow = (wm * TM * 16 + l16) * kStepK + place, wrow = (BM + wn * TN * 16 + l16) * kStepK + place;
   i32x4 acc[TM][TN] = {};
-  i32x4 xa[TM], wa[TN], xb[TM], wb[TN];
-  const auto fetch = [&](int step, i32x4 (&xf)[TM], i32x4 (&wf)[TN]) __attribute__((always_inline)) {
-    const char* from = lds[(unsigned)step % kStages];
+  i32x4 xf[TM], wf[TN];
+  // Step s: the step kStages - 1 ahead is requested into the place of the step before, which the other
+  // waves have read.
+  const auto run = [&](auto inner, int s) __attribute__((always_inline)) {
+    constexpr bool kInner = decltype(inner)::value;  // kStages - 1 steps or more follow
+    const char* from = lds[s % kStages];
+    if (kInner || s + kStages - 1 < last) fill(s + kStages - 1);
 #pragma unroll
     for (int j = 0; j < TN; ++j) wf[j] = *(const i32x4*)(from + wrow + j * 16 * kStepK);
 #pragma unroll
     for (int i = 0; i < TM; ++i) xf[i] = *(const i32x4*)(from + xrow + i * 16 * kStepK);
-  };
-  // Step s: its fragments are in registers and its place in LDS is free, so the step kStages ahead is
-  // requested into it; the next step's fragments are read while this one's are multiplied.
-  const auto run = [&](auto inner, int s, i32x4 (&xf)[TM], i32x4 (&wf)[TN], i32x4 (&xn)[TM], i32x4 (&wn)[TN])
-                       __attribute__((always_inline)) {
-    constexpr bool kInner = decltype(inner)::value;  // kStages steps or more follow
-    if (kInner || s + kStages - 1 < last) wait_and_meet<(kStages - 2) * (LX + LW)>();
-    else wait_and_meet<0>();
-    if (kInner || s + kStages < last) fill(s + kStages);
-    if (kInner || s + 1 < last) fetch(s + 1, xn, wn);
+    if (kInner) end_reading<(kStages - 2) * (LX + LW)>();  // the next step's loads are done
+    else end_reading<0>();
     if (!kInner && chunks - s * 4 < 4) {  // the end of the rows
 #pragma unroll
       for (int j = 0; j < TN; ++j)
         if (l4 >= chunks - s * 4) wf[j] = i32x4{0, 0, 0, 0};
     }
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[j], xf[i], acc[i][j], 0, 0, 0);
+    __builtin_amdgcn_s_setprio(0);
+    meet();
   };
-  if (first < last) {
+  const bool behind = W == 8 && wave >= 4;
 #pragma unroll
-    for (int k = 0; k < kStages; ++k)
-      if (first + k < last) fill(first + k);
-    wait_and_meet<0>();
-    fetch(first, xa, wa);
-    int s = first;
-    for (; s + 1 + kStages < last; s += 2) {
-      run(std::true_type(), s, xa, wa, xb, wb);
-      run(std::true_type(), s + 1, xb, wb, xa, wa);
-    }
-    for (; s < last; s += 2) {
-      run(std::false_type(), s, xa, wa, xb, wb);
-      if (s + 1 < last) run(std::false_type(), s + 1, xb, wb, xa, wa);
-    }
-  }
+  for (int k = 0; k < kStages - 1; ++k)
+    if (first + k < last) fill(first + k);
+  end_reading<0>();
+  if (behind) meet();
+  int s = first;
+  for (; s + kStages - 1 < last; ++s) run(std::true_type(), s);
+  for (; s < last; ++s) run(std::false_type(), s);
+  if (W == 8 && !behind) meet();
 
   // a lane has, of row m0 + lane % 16 of each 16, the channels n to n + 15
   const int64_t n = n0 + wn * 64 + l4 * 16;
@@ -324,11 +329,25 @@ __global__ void __launch_bounds__(WI* WJ * 64, 2) grad_kernel(GradArgs g, uint32
   constexpr int TI = BI / WI / 16, TJ = BJ / WJ / 16;
   constexpr int LA = BI * S / 8 / T, LQ = BJ * S / 16 / T;  // 16-byte chunks of a thread
   constexpr int TERMS = FEED == kScaled ? 2 : 1;
-  constexpr int ABYTES = BI * S * 2, STEP = ABYTES * TERMS + BJ * S * 2;
-  constexpr int kStages = FEED == kDirect ? 4 : 3;  // tile steps in LDS
+  constexpr int ABYTES = BI * S * 2;
+  constexpr int kStages = FEED == kDirect ? 4 : 2;  // tile steps in LDS
   static_assert(BI * S / 8 % T == 0 && BJ * S / 16 % T == 0, "whole chunks");
   static_assert(TJ == 4, "a lane's results of a row are 16 consecutive ones");
-  __shared__ __attribute__((aligned(1024))) char lds[kStages][STEP];
+  // Each step's place is a variable of its own, named at compile time: the compiler would have a
+  // transposing read wait for every load into the variable that it reads from.
+  __shared__ __attribute__((aligned(1024))) char a0[ABYTES * TERMS], a1[ABYTES * TERMS], a2[kStages > 2 ? ABYTES : 16],
+      a3[kStages > 2 ? ABYTES : 16], q0[BJ * S * 2], q1[BJ * S * 2];
+  const auto a_place = [&](auto k) __attribute__((always_inline)) {
+    constexpr int K = decltype(k)::value % kStages;
+    if constexpr (K == 0) return (char*)a0;
+    else if constexpr (K == 1) return (char*)a1;
+    else if constexpr (K == 2) return (char*)a2;
+    else return (char*)a3;
+  };
+  const auto q_place = [&](auto k) __attribute__((always_inline)) {
+    if constexpr (decltype(k)::value % 2 == 0) return (char*)q0;
+    else return (char*)q1;
+  };
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const Tile tile = tile_of(blockIdx.x, tiles_i, tiles_j);
   const int64_t i0 = tile.i * BI, j0 = tile.j * BJ;
@@ -350,13 +369,13 @@ __global__ void __launch_bounds__(WI* WJ * 64, 2) grad_kernel(GradArgs g, uint32
       }
     }
   }
-  const auto fill = [&](auto inner, int step) __attribute__((always_inline)) {
+  const auto fill = [&](auto inner, auto k, int step) __attribute__((always_inline)) {
     const int64_t s0 = (int64_t)step * S;
     const char* base = (const char*)g.a.p + (TRANS ? s0 * g.a.pitch + i0 : i0 * g.a.pitch + s0) * 2;
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, 0xFFFFFFFFu, 0x00020000);
     // past the end of s the last row or chunk is read; multiply() leaves it out
     const int over = (int)(s0 + S - g.nc);
-    char* to = lds[(unsigned)step % kStages];
+    char* to = a_place(k);
 #pragma unroll
     for (int u = 0; u < LA; ++u) {
       uint32_t o = at[u];
@@ -436,9 +455,9 @@ __global__ void __launch_bounds__(WI* WJ * 64, 2) grad_kernel(GradArgs g, uint32
       }
     }
   };
-  const auto stage = [&](int step, Held& h) __attribute__((always_inline)) {
-    char* la = lds[(unsigned)step % kStages];
-    char* lq = la + ABYTES * TERMS;
+  const auto stage = [&](auto k, Held& h) __attribute__((always_inline)) {
+    [[maybe_unused]] char* la = a_place(k);
+    char* lq = q_place(k);
     if constexpr (FEED != kDirect) {
 #pragma unroll
       for (int u = 0; u < LA; ++u) {
@@ -499,40 +518,50 @@ __global__ void __launch_bounds__(WI* WJ * 64, 2) grad_kernel(GradArgs g, uint32
   const int trow = l4 * 8 + (l16 >> 2), tcol = (l16 & 3) * 8, tswz = seg_swizzle(trow);
   f32x4 acc[TI][TJ] = {};
   bf16x8 fa[TERMS][TI], fq[TJ];
-  const auto frag_t = [&](const char* base, int width, int seg) __attribute__((always_inline)) {
-    const char* p = base + trow * width * 2 + ((seg ^ tswz) << 5) + tcol;
+  constexpr int NA = TRANS ? (TI < 8 ? TI : 8) : 1;
+  int a_at[NA], q_at[TJ];  // of a wave's segments
+#pragma unroll
+  for (int k = 0; k < NA; ++k) a_at[k] = trow * BI * 2 + (((wi * TI + k) ^ tswz) << 5) + tcol;
+#pragma unroll
+  for (int k = 0; k < TJ; ++k) q_at[k] = trow * BJ * 2 + (((wj * TJ + k) ^ tswz) << 5) + tcol;
+  static_assert(TI <= 8, "one address for each");
+  const int a_row = ((wi * TI) * 16 + l16) * S * 2 + ((l4 ^ (-(l16 >> 2) & 3)) << 4);
+  const auto frag_t = [&](char* base, int at, int width) __attribute__((always_inline)) {
+    ZS_LDS(char)* p = (ZS_LDS(char)*)base + at;
     const bf16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((ZS_LDS(bf16x4)*)p);
     const bf16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((ZS_LDS(bf16x4)*)(p + 4 * width * 2));
     return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
   };
-  const auto fetch_q = [&](int step, int j) __attribute__((always_inline)) {
-    return frag_t(lds[(unsigned)step % kStages] + ABYTES * TERMS, BJ, wj * TJ + j);
+  const auto fetch_q = [&](auto k, int j) __attribute__((always_inline)) { return frag_t(q_place(k), q_at[j], BJ); };
+  const auto fetch_a = [&](auto k, int h, int i) __attribute__((always_inline)) {
+    char* la = a_place(k) + h * ABYTES;
+    if constexpr (TRANS) return frag_t(la, a_at[i], BI);
+    else return *(const bf16x8*)(la + a_row + i * 16 * S * 2);
   };
-  const auto fetch_a = [&](int step, int h, int i) __attribute__((always_inline)) {
-    const char* la = lds[(unsigned)step % kStages] + h * ABYTES;
-    if constexpr (TRANS) return frag_t(la, BI, wi * TI + i);
-    else return *(const bf16x8*)(la + ((wi * TI + i) * 16 + l16) * S * 2 + ((l4 ^ (-(l16 >> 2) & 3)) << 4));
-  };
-  // Step s: its fragments of a and the first two of q are in registers; the last two are read while the
-  // first are multiplied, then the next step's into the registers that the products are done with.
-  // The step before has left its place in LDS to the step three ahead (a, loaded into it); the step
-  // two ahead is converted into its place, and the one four ahead requested into the
-  // registers that it leaves.
-  const auto run = [&](auto inner, int s, Held& h) __attribute__((always_inline)) {
-    constexpr bool kInner = decltype(inner)::value;  // five steps or more follow
-    constexpr int kLoads = LA + 2 * LQ;              // of a step, where a is loaded into LDS
-    const bool more = kInner || s + 1 < last;
+  // Step s: the step three ahead is requested into the place of the step before, which the other waves
+  // have read (a, loaded into LDS), and into registers (the rest); the step ahead, requested two steps
+  // before, is converted into its place.
+  const auto run = [&](auto inner, auto k, int s) __attribute__((always_inline)) {
+    constexpr bool kInner = decltype(inner)::value;  // four steps or more follow
+    constexpr int K = decltype(k)::value;            // s - first, modulo 4
+    Held& h = held[(K + 1) % 2];
     if constexpr (FEED == kDirect) {
-      if (kInner || s + 2 < last) wait_and_meet<kLoads + 2 * LQ>();
-      else wait_and_meet<0>();
-      if (kInner || s + 3 < last) fill(inner, s + 3);
-    } else {
-      wait_and_meet<63>();
+      if (kInner || s + 3 < last) fill(inner, std::integral_constant<int, (K + 3) % 4>(), s + 3);
     }
-    fq[2] = fetch_q(s, 2);
-    fq[3] = fetch_q(s, 3);
-    if (kInner || s + 2 < last) stage(s + 2, h);
-    if (kInner || s + 4 < last) load(inner, s + 4, h);
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) fq[j] = fetch_q(k, j);
+#pragma unroll
+    for (int h2 = 0; h2 < TERMS; ++h2)
+#pragma unroll
+      for (int i = 0; i < TI; ++i) fa[h2][i] = fetch_a(k, h2, i);
+    if (kInner || s + 1 < last) stage(std::integral_constant<int, (K + 1) % 4>(), h);
+    if (kInner || s + 3 < last) load(inner, s + 3, h);
+    if constexpr (FEED == kDirect) {  // the next step's loads into LDS are done
+      if (kInner) end_reading<2 * (LA + 2 * LQ) + 2 * LQ>();
+      else end_reading<0>();
+    } else {
+      end_reading<63>();
+    }
     if constexpr (FEED == kDirect) {
       if (!kInner && (int64_t)(s + 1) * S > g.nc) {  // rows of s past the end
         const int left = (int)(g.nc - (int64_t)s * S) - l4 * 8;
@@ -545,54 +574,50 @@ __global__ void __launch_bounds__(WI* WJ * 64, 2) grad_kernel(GradArgs g, uint32
         }
       }
     }
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int h2 = 0; h2 < TERMS; ++h2)
 #pragma unroll
-      for (int h2 = 0; h2 < TERMS; ++h2)
+      for (int i = 0; i < TI; ++i)
 #pragma unroll
-        for (int i = 0; i < TI; ++i) {
-#pragma unroll
-          for (int j = 2 * half; j < 2 * half + 2; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[j], fa[h2][i], acc[i][j], 0, 0, 0);
-          if (half == 1 && more) fa[h2][i] = fetch_a(s + 1, h2, i);
-        }
-      if (half == 0 && more) {
-        fq[0] = fetch_q(s + 1, 0);
-        fq[1] = fetch_q(s + 1, 1);
-      }
-    }
+        for (int j = 0; j < TJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[j], fa[h2][i], acc[i][j], 0, 0, 0);
+    __builtin_amdgcn_s_setprio(0);
+    meet();
   };
-  if (first < last) {
-    if constexpr (FEED == kDirect) {
-#pragma unroll
-      for (int k = 0; k < 3; ++k)
-        if (first + k < last) fill(std::false_type(), first + k);
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (first + k < last) load(std::false_type(), first + k, held[k]);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (first + k < last) stage(first + k, held[k]);
-      if (first + 2 + k < last) load(std::false_type(), first + 2 + k, held[k]);
-    }
-    wait_and_meet<0>();
-    fq[0] = fetch_q(first, 0);
-    fq[1] = fetch_q(first, 1);
-#pragma unroll
-    for (int h = 0; h < TERMS; ++h)
-#pragma unroll
-      for (int i = 0; i < TI; ++i) fa[h][i] = fetch_a(first, h, i);
-    int s = first;
-    for (; s + 6 < last; s += 2) {
-      run(std::true_type(), s, held[0]);
-      run(std::true_type(), s + 1, held[1]);
-    }
-    for (; s < last; s += 2) {
-      run(std::false_type(), s, held[0]);
-      if (s + 1 < last) run(std::false_type(), s + 1, held[1]);
-    }
+  const bool behind = W == 8 && wave >= 4;
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  using I3 = std::integral_constant<int, 3>;
+  using Any = std::false_type;
+  using Inner = std::true_type;
+  if constexpr (FEED == kDirect) {
+    if (first < last) fill(Any(), I0(), first);
+    if (first + 1 < last) fill(Any(), I1(), first + 1);
+    if (first + 2 < last) fill(Any(), I2(), first + 2);
   }
+  if (first < last) {
+    load(Any(), first, held[0]);
+    stage(I0(), held[0]);
+  }
+  if (first + 1 < last) load(Any(), first + 1, held[1]);
+  if (first + 2 < last) load(Any(), first + 2, held[0]);
+  end_reading<0>();
+  if (behind) meet();
+  int s = first;
+  for (; s + 7 < last; s += 4) {
+    run(Inner(), I0(), s);
+    run(Inner(), I1(), s + 1);
+    run(Inner(), I2(), s + 2);
+    run(Inner(), I3(), s + 3);
+  }
+  for (; s < last; s += 4) {
+    run(Any(), I0(), s);
+    if (s + 1 < last) run(Any(), I1(), s + 1);
+    if (s + 2 < last) run(Any(), I2(), s + 2);
+    if (s + 3 < last) run(Any(), I3(), s + 3);
+  }
+  if (W == 8 && !behind) meet();
 
   // a lane has, of row lane % 16 of each 16, the columns c to c + 15
   const int64_t c = j0 + wj * 64 + l4 * 16;
