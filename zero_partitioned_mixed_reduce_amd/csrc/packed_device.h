@@ -65,6 +65,31 @@ __device__ __forceinline__ float get(const Raw8<DT>& r, int i) {  // i known at 
   if constexpr (DT == ZERO_F32) return __uint_as_float(r.v[i >> 2][i & 3]);
   else return (i & 1) ? dec_hi<DT>(r.v[0][i >> 1]) : dec_lo<DT>(r.v[0][i >> 1]);
 }
+// Largest magnitude of the elements, and of m: for a 16-bit type two at a time, as bit patterns side by
+// side, which are ordered as the magnitudes are.
+template <int DT>
+__device__ __forceinline__ uint32_t max_raw(const Raw8<DT>& r, uint32_t m) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+  for (int i = 0; i < 2 * esize(DT); ++i) {
+    if constexpr (DT == ZERO_F32) {
+      const uint32_t a = r.v[i >> 2][i & 3] & 0x7FFFFFFFu;
+      m = m > a ? m : a;
+    } else {
+      const u16x2 a = __builtin_bit_cast(u16x2, r.v[0][i] & 0x7FFF7FFFu);
+      m = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, m), a));
+    }
+  }
+  return m;
+}
+// ... as the bits of a float.
+template <int DT>
+__device__ __forceinline__ uint32_t max_bits(uint32_t m) {
+  if constexpr (DT == ZERO_F32) return m;
+  const uint32_t a = m & 0xFFFFu, b = m >> 16;
+  return __float_as_uint(dec_lo<DT>(a > b ? a : b));
+}
+
 // Elements [c, c + 8) of a row of `cols`; zeros past its end (and before its start, never read).
 template <int DT>
 __device__ __forceinline__ Raw8<DT> load8(const char* row, int64_t c, int64_t cols) {
@@ -138,28 +163,33 @@ __device__ __forceinline__ Rounding rounding(uint32_t top) {
   if (r.none) r.scale = top == 0 ? 0.0f : __uint_as_float(0x7FC00000u);
   return r;
 }
-// Nearest integer to x / scale, to even between two.  x * inv is exact for powers of two; for
-// others it is within a step of the answer, and the sign of what is left over, an exact
-// difference, says which: x and k * scale are multiples of half of scale's last place, and the
-// difference is at most about scale / 2, which 24 bits hold.
+// The nearest integer to x / scale, to even between two, in the last byte.  x * inv is exact for powers
+// of two, and added to 1.5 * 2^23 is rounded once, to a whole number whose two's complement the
+// result's low bits are.  For others it is within a step of the answer, and the sign of what is
+// left over, an exact difference, says which: x and k * scale are multiples of half of scale's last
+// place, and the difference is at most about scale / 2, which 24 bits hold.
 template <int RULE>
-__device__ __forceinline__ int quantise(float x, const Rounding& r) {
-  if (r.none) return 0;
+__device__ __forceinline__ uint32_t quantise(float x, const Rounding& r) {
+  constexpr float kWhole = 12582912.0f;
+  if constexpr (RULE == ZERO_SCALE_POW2) return __float_as_uint(__builtin_fmaf(x, r.inv, kWhole));
   float k = rintf(x * r.inv);
-  if constexpr (RULE == ZERO_SCALE_MAX) {
-    const float d = __builtin_fmaf(-k, r.scale, x);
-    const float t = 2.0f * __builtin_fabsf(d);
-    const bool odd = (int)k & 1;
-    if (t > r.scale || (t == r.scale && odd)) k += __builtin_copysignf(1.0f, d);
-    k = fminf(fmaxf(k, -127.0f), 127.0f);
-  }
-  return (int)k;
+  const float d = __builtin_fmaf(-k, r.scale, x);
+  const float t = 2.0f * __builtin_fabsf(d);
+  const bool odd = (int)k & 1;
+  if (t > r.scale || (t == r.scale && odd)) k += __builtin_copysignf(1.0f, d);
+  return __float_as_uint(fminf(fmaxf(k, -127.0f), 127.0f) + kWhole);
 }
 template <int RULE>
 __device__ __forceinline__ u32x2 quantise8(const float (&x)[8], const Rounding& r) {
-  u32x2 o = {0, 0};
+  u32x2 o;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o[i >> 2] |= ((uint32_t)quantise<RULE>(x[i], r) & 0xFFu) << (8 * (i & 3));
+  for (int h = 0; h < 2; ++h) {
+    uint32_t b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = quantise<RULE>(x[4 * h + i], r);
+    const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400), hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0c);
+    o[h] = r.none ? 0u : lo | hi;
+  }
   return o;
 }
 

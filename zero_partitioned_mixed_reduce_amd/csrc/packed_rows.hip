@@ -77,11 +77,8 @@ __global__ void __launch_bounds__(kRowBlock<T>) write_kernel(MatArg x, PackArg p
         raw[u] = load8<DT>(src, c, cols);
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        decode8<DT>(raw[u], v);
-        m = max8(v, m);
-      }
-      const Rounding k = rounding<RULE>(row_max<T>(m, lds));
+      for (int u = 0; u < U; ++u) m = max_raw<DT>(raw[u], m);
+      const Rounding k = rounding<RULE>(row_max<T>(max_bits<DT>(m), lds));
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t c = 8 * (int64_t)(t + u * T);
@@ -90,11 +87,8 @@ __global__ void __launch_bounds__(kRowBlock<T>) write_kernel(MatArg x, PackArg p
       }
       if (t == 0) p.scale[r] = k.scale;
     } else {
-      for (int64_t c = 8 * t; c < cols; c += 8 * T) {
-        decode8<DT>(load8<DT>(src, c, cols), v);
-        m = max8(v, m);
-      }
-      const Rounding k = rounding<RULE>(row_max<T>(m, lds));
+      for (int64_t c = 8 * t; c < cols; c += 8 * T) m = max_raw<DT>(load8<DT>(src, c, cols), m);
+      const Rounding k = rounding<RULE>(row_max<T>(max_bits<DT>(m), lds));
       for (int64_t c = 8 * t; c < wide; c += 8 * T) {
         decode8<DT>(load8<DT>(src, c, cols), v);
         *(u32x2*)(dst + c) = quantise8<RULE>(v, k);
@@ -127,32 +121,23 @@ __global__ void __launch_bounds__(256) read_kernel(PackArg p, MatArg out, int64_
 // ---------------------------------------------------------------------------
 // Activation functions
 
-// exp(x) to about one unit in the last place: the product with log2(e) in two parts.
-__device__ __forceinline__ float exp_of(float x) {
-  const float hi = x * 1.44269502162933349609375f;
-  float lo = __builtin_fmaf(x, 1.44269502162933349609375f, -hi);
-  lo = __builtin_fmaf(x, 1.925963033500011079e-08f, lo);
-  const float e = __builtin_amdgcn_exp2f(hi);
-  // beyond the range the parts are not finite
-  return __builtin_fabsf(x) < 88.0f ? __builtin_fmaf(e, lo * 0.693147182464599609375f, e) : e;
-}
-
 // f(x) = x g(h(x)), g the logistic function; f' = g + x g (1 - g) h'.
 template <int KIND>
 __device__ __forceinline__ void curve(float x, float& f, float& slope) {
-  // far out g is 0 or 1 and does not change any more; there h stays finite
-  const float z = fminf(fmaxf(x, -1e4f), 1e4f);
-  float h, dh;
+  float h = x, dh = 1.0f;
   if constexpr (KIND == ZERO_ACT_GELU) {
     constexpr float a = 1.5957691216057308f, b = 0.044715f * 1.5957691216057308f;  // 2 sqrt(2 / pi)
-    const float z2 = z * z;
-    h = z * __builtin_fmaf(b, z2, a);
-    dh = __builtin_fmaf(3.0f * b, z2, a);
-  } else {
-    h = z;
-    dh = 1.0f;
+    const float x2 = x * x;
+    h = x * __builtin_fmaf(b, x2, a);
+    dh = fminf(__builtin_fmaf(3.0f * b, x2, a), 1e30f);  // times 0 where it would be infinite
   }
-  const float e = exp_of(-h);
+  // e^-h; beyond 104 it is 0 or infinite, and g is 1 or 0.  The product with log2(e) in two parts, so
+  // that the power is right to about a unit in the last place.
+  h = __builtin_amdgcn_fmed3f(h, -104.0f, 104.0f);
+  const float hi = h * -1.44269502162933349609375f;
+  float lo = __builtin_fmaf(h, -1.44269502162933349609375f, -hi);
+  lo = __builtin_fmaf(h, -1.925963033500011079e-08f, lo);
+  const float e = __builtin_amdgcn_exp2f(hi) * __builtin_fmaf(lo, 0.693147182464599609375f, 1.0f);
   const float g = __builtin_amdgcn_rcpf(1.0f + e);
   f = x * g;
   // 1 - g = e g, without cancellation; e is infinite where g is 0
@@ -195,44 +180,39 @@ __global__ void __launch_bounds__(kRowBlock<T>) act_kernel(MatArg x, PackArg xp,
     // a thread's groups of eight: in registers (U > 0), or loaded anew
     constexpr int H = U > 0 ? U : 1;
     Raw8<DT> a[H], b[H];
+    float vy[H][8];
     const auto fetch = [&](int u, int64_t c) __attribute__((always_inline)) {
       a[u] = load8<DT>(src, c, n);
       if constexpr (GATED) b[u] = load8<DT>(src2, c, n);
     };
-    const auto compute = [&](int u, float (&va)[8], float (&vb)[8], float (&vy)[8]) __attribute__((always_inline)) {
-      decode8<DT>(a[u], va);
-      if constexpr (GATED) decode8<DT>(b[u], vb);
+    const auto compute = [&](int u) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        vy[i] = value<KIND>(va[i]);
-        if constexpr (GATED) vy[i] *= vb[i];
+        vy[u][i] = value<KIND>(get<DT>(a[u], i));
+        if constexpr (GATED) vy[u][i] *= get<DT>(b[u], i);
       }
     };
-    float va[8], vb[8], vy[8];
     const auto first = [&](int u) __attribute__((always_inline)) {
-      if (yp.q) {
-        compute(u, va, vb, vy);
-        my = max8(vy, my);
-      } else {
-        decode8<DT>(a[u], va);
-        if constexpr (GATED) decode8<DT>(b[u], vb);
-      }
-      mx = max8(va, mx);
-      if constexpr (GATED) mx = max8(vb, mx);
+      if (yp.q) my = max8(vy[u], my);
+      mx = max_raw<DT>(a[u], mx);
+      if constexpr (GATED) mx = max_raw<DT>(b[u], mx);
     };
     if constexpr (U > 0) {
 #pragma unroll
       for (int u = 0; u < U; ++u) fetch(u, 8 * (int64_t)(t + u * T));
-      if (xp.q || yp.q) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) first(u);
+      for (int u = 0; u < U; ++u) {
+        compute(u);
+        first(u);
       }
     } else if (xp.q || yp.q) {
       for (int64_t c = 8 * t; c < n; c += 8 * T) {
         fetch(0, c);
+        compute(0);
         first(0);
       }
     }
+    mx = max_bits<DT>(mx);
     Rounding kx{}, ky{};
     if (xp.q) kx = xp.rule == ZERO_SCALE_POW2 ? rounding<ZERO_SCALE_POW2>(row_max<T>(mx, lds))
                                               : rounding<ZERO_SCALE_MAX>(row_max<T>(mx, lds));
@@ -244,14 +224,16 @@ __global__ void __launch_bounds__(kRowBlock<T>) act_kernel(MatArg x, PackArg xp,
       return rule == ZERO_SCALE_POW2 ? quantise8<ZERO_SCALE_POW2>(v, k) : quantise8<ZERO_SCALE_MAX>(v, k);
     };
     const auto second = [&](int u, int64_t c) __attribute__((always_inline)) {
-      compute(u, va, vb, vy);
-      if (c < n && y.p) store_y(y, r, c, n, vy);
+      if (c < n && y.p) store_y(y, r, c, n, vy[u]);
       if (xp.q) {
-        const u32x2 wa = put(va, kx, xp.rule);
+        float v[8];
+        decode8<DT>(a[u], v);
+        const u32x2 wa = put(v, kx, xp.rule);
         if (!GATED) {
           if (c < wide) *(u32x2*)(qx + c) = wa;
         } else {
-          const u32x2 wb = put(vb, kx, xp.rule);
+          decode8<DT>(b[u], v);
+          const u32x2 wb = put(v, kx, xp.rule);
           if (together) {
             if (c < n) *(u32x2*)(qx + c) = wa, *(u32x2*)(qx + n + c) = wb;
           } else {
@@ -264,7 +246,7 @@ __global__ void __launch_bounds__(kRowBlock<T>) act_kernel(MatArg x, PackArg xp,
           }
         }
       }
-      if (yp.q && c < wide) *(u32x2*)(qy + c) = put(vy, ky, yp.rule);
+      if (yp.q && c < wide) *(u32x2*)(qy + c) = put(vy[u], ky, yp.rule);
     };
     if constexpr (U > 0) {
 #pragma unroll
@@ -272,6 +254,7 @@ __global__ void __launch_bounds__(kRowBlock<T>) act_kernel(MatArg x, PackArg xp,
     } else {
       for (int64_t c = 8 * t; c < wide; c += 8 * T) {
         fetch(0, c);
+        compute(0);
         second(0, c);
       }
     }
@@ -347,14 +330,17 @@ static int64_t row_grid(int64_t rows) {
 template <class F>
 static void by_length(int64_t cols, F fn) {
   const int64_t groups = (cols + 15) / 16 * 2;
-  if (groups <= 64) fn(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
-  else if (groups <= 128) fn(std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
-  else if (groups <= 256) fn(std::integral_constant<int, 64>(), std::integral_constant<int, 4>());
-  else if (groups <= 512) fn(std::integral_constant<int, 256>(), std::integral_constant<int, 2>());
-  else if (groups <= 1024) fn(std::integral_constant<int, 256>(), std::integral_constant<int, 4>());
-  else if (groups <= 2048) fn(std::integral_constant<int, 512>(), std::integral_constant<int, 4>());
-  else if (groups <= 4096) fn(std::integral_constant<int, 1024>(), std::integral_constant<int, 4>());
-  else fn(std::integral_constant<int, 1024>(), std::integral_constant<int, 0>());
+  using std::integral_constant;
+  if (groups <= 64) fn(integral_constant<int, 64>(), integral_constant<int, 1>());
+  else if (groups <= 128) fn(integral_constant<int, 64>(), integral_constant<int, 2>());
+  else if (groups <= 256) fn(integral_constant<int, 64>(), integral_constant<int, 4>());
+  else if (groups <= 512) fn(integral_constant<int, 256>(), integral_constant<int, 2>());
+  else if (groups <= 768) fn(integral_constant<int, 256>(), integral_constant<int, 3>());
+  else if (groups <= 1024) fn(integral_constant<int, 256>(), integral_constant<int, 4>());
+  else if (groups <= 1536) fn(integral_constant<int, 512>(), integral_constant<int, 3>());
+  else if (groups <= 2048) fn(integral_constant<int, 512>(), integral_constant<int, 4>());
+  else if (groups <= 4096) fn(integral_constant<int, 1024>(), integral_constant<int, 4>());
+  else fn(integral_constant<int, 1024>(), integral_constant<int, 0>());
 }
 template <class F>
 static void by_dtype(int32_t dt, F fn) {
