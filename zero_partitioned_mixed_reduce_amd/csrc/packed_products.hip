@@ -1,5 +1,6 @@
 // gfx950 kernels of the packed rows' products: the linear layer in 8-bit integers, and the products
 // of a 16-bit matrix with packed rows whose scales lie along the sum (weight and input gradients).
+#include <cmath>
 #include <type_traits>
 
 #include "packed_device.h"
@@ -272,6 +273,68 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) linear_kernel(LinearArgs a, ui
     }
   });
 #endif
+}
+
+// A few tokens (16 MT at most), bound by the bytes of w: a block takes 16 channels, and its W waves every
+// W-th run of 128 of k, whose integer sums they join.  Nothing goes through LDS before that: a
+// lane's 32 bytes of a run are the operands of two instructions, whose k are numbered alike in x
+// and w.
+template <int MT, int W>
+__global__ void __launch_bounds__(W * 64) linear_few_kernel(LinearArgs a) {
+  __shared__ i32x4 lds[W][MT][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int l16 = lane & 15, l4 = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int chunks = (int)((a.k + 15) >> 4), runs = (chunks + 7) >> 3;
+  const int8_t* w = a.w.q + (n0 + l16 < a.n ? n0 + l16 : a.n - 1) * a.w.pitch;
+  const int8_t* x[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) x[i] = a.x.q + (i * 16 + l16 < a.m ? i * 16 + l16 : a.m - 1) * a.x.pitch;
+  i32x4 acc[MT] = {};
+  constexpr int U = 4 / MT;  // runs whose loads are under way at once
+  const auto take = [&](auto whole, int r0) __attribute__((always_inline)) {
+    constexpr bool kWhole = decltype(whole)::value;  // U runs, no end of the rows among them
+    i32x4 wf[U][2], xf[U][2][MT];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        int c = (r0 + u * W) * 8 + l4 * 2 + h;
+        if (!kWhole) c = c < chunks ? c : chunks - 1;
+        wf[u][h] = *(const i32x4*)(w + c * 16);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) xf[u][h][i] = *(const i32x4*)(x[i] + c * 16);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (!kWhole && (r0 + u * W) * 8 + l4 * 2 + h >= chunks) wf[u][h] = i32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[u][h], xf[u][h][i], acc[i], 0, 0, 0);
+      }
+  };
+  int r = wave;
+  for (; (r + (U - 1) * W + 1) * 8 <= chunks; r += U * W) take(std::true_type(), r);
+  for (; r < runs; r += U * W) take(std::false_type(), r);
+#pragma unroll
+  for (int i = 0; i < MT; ++i) lds[wave][i][lane] = acc[i];
+  __syncthreads();
+  if (wave >= MT) return;
+  i32x4 sum = lds[0][wave][lane];
+#pragma unroll
+  for (int k = 1; k < W; ++k) sum += lds[k][wave][lane];
+  const int64_t m = wave * 16 + l16, n = n0 + l4 * 4;
+  if (m >= a.m || n >= a.n) return;
+  const Channels<4> ch(a, n);
+  const float xs = a.x.scale[m];
+  float v[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = ch(k, sum[k], xs);
+  with_type(a.y.dtype, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    store_run<DT, 4>((char*)a.y.p + m * a.y.pitch * esize(DT), n, a.n, v);
+  });
 }
 
 // Adds the splits' integer sums, which no order changes.
@@ -714,7 +777,10 @@ static int64_t join_grid(int64_t quads) {
 }
 
 // Tiles of `bi` x `bj` and a contraction of `steps`: split until the chip's 256 compute units have a
-// block each, but no finer than four steps to a split.
+// block each (of the small tiles two), but no finer than four steps to a split, and not beyond where
+// what the splits write and the join reads takes longer than the steps saved: a step takes about
+// 0.35 us, and a split about 2 ps for each result, so the sum is least at the root of their ratio
+// (128 tokens of 4096 x 4096: 16 splits 30 us, 4 splits 18).
 static ProductPlan plan_product(int64_t ni, int64_t nj, int64_t steps, int64_t bi, int64_t bj, int64_t elem) {
   ProductPlan p{};
   p.tile = (int32_t)bi;
@@ -722,20 +788,46 @@ static ProductPlan plan_product(int64_t ni, int64_t nj, int64_t steps, int64_t b
   p.tiles_j = up(nj, bj);
   p.steps = steps;
   const int64_t tiles = p.tiles_i * p.tiles_j;
-  int64_t s = tiles > 0 ? 256 / tiles : 1;
+  int64_t s = tiles > 0 ? (bi == 128 ? 512 : 256) / tiles : 1;  // of the small tiles two at a time
   if (s > steps / 4) s = steps / 4;
+  const int64_t least = (int64_t)std::sqrt(175000.0 * (double)steps / ((double)ni * (double)nj + 1.0));
+  if (s > least) s = least;
   if (s < 1) s = 1;
   p.splits = up(steps > 0 ? steps : 1, up(steps > 0 ? steps : 1, s));
   p.ws_bytes = p.splits > 1 ? p.splits * ni * (up(nj, 4) * 4) * elem : 0;
   return p;
 }
 
+constexpr int64_t kFewTokens = 64;  // the most that linear_few_kernel takes
+
 ProductPlan plan_linear(int64_t m, int64_t k, int64_t n) {
+  if (m <= kFewTokens) {
+    ProductPlan few = plan_product(m, n, 1, kFewTokens, 16, 4);
+    few.tile = 16;
+    few.splits = 1;
+    few.ws_bytes = 0;
+    return few;
+  }
   const ProductPlan p = plan_product(m, n, up(k, kStepK), 256, 256, 4);
   return p.tiles_i * p.tiles_j >= 256 ? p : plan_product(m, n, up(k, kStepK), 128, 128, 4);
 }
 
+// Four waves to 16 channels fill the chip from 8192 channels on; fewer channels take more waves each.
+template <int MT>
+static void launch_linear_few(const LinearArgs& a, hipStream_t st) {
+  const uint32_t grid = (uint32_t)up(a.n, 16);
+  if (a.n >= 8192) linear_few_kernel<MT, 4><<<grid, 256, 0, st>>>(a);
+  else if (a.n >= 2048) linear_few_kernel<MT, 8><<<grid, 512, 0, st>>>(a);
+  else linear_few_kernel<MT, 16><<<grid, 1024, 0, st>>>(a);
+}
+
 hipError_t launch_linear(const LinearArgs& a, const ProductPlan& p, hipStream_t st) {
+  if (p.tile == 16) {
+    if (a.m <= 16) launch_linear_few<1>(a, st);
+    else if (a.m <= 32) launch_linear_few<2>(a, st);
+    else launch_linear_few<4>(a, st);
+    return hipGetLastError();
+  }
   const dim3 grid((uint32_t)(p.tiles_i * p.tiles_j), (uint32_t)p.splits);
   if (p.tile == 256) linear_kernel<256, 256, 2, 4, 4><<<grid, 512, 0, st>>>(a, (uint32_t)p.tiles_i, (uint32_t)p.tiles_j, p.steps, up(p.steps, p.splits));
   else linear_kernel<128, 128, 2, 2, 4><<<grid, 256, 0, st>>>(a, (uint32_t)p.tiles_i, (uint32_t)p.tiles_j, p.steps, up(p.steps, p.splits));
