@@ -331,6 +331,21 @@ def test_gradients_of_infinities(dtype, rule):
     assert w.zero_packed_input_grad(dy).isnan().all()
 
 
+@pytest.mark.parametrize("e", [-126, -100, 104, 112, 121, 122])
+def test_gradients_of_extreme_scales(e):
+    """Scales from the smallest to the largest there are: the products q * scale are finite, and exact."""
+    m, k, n = 45, 70, 33
+    top = 63 if e == 122 else 127                       # 127 * 2^122 is no float
+    x = random_packed(m, k, 1, POW2, torch.full((m,), 2.0 ** e, device=DEV))
+    x._q.clamp_(-top, top)
+    assert torch.equal(x.zero_packed_read(dtype=F32).double(), values(x)) and values(x).abs().max() < 3.4e38
+    dy = whole_dy(m, n, BF16, 5) * 2.0 ** (-e // 2)
+    assert torch.equal(x.zero_packed_weight_grad(dy).double(), dy.double().T @ values(x))
+    w = x
+    dz = whole_dy(n, m, BF16, 6) * 2.0 ** (-e // 2)
+    assert torch.equal(w.zero_packed_input_grad(dz, dtype=F32).double(), dz.double() @ values(w))
+
+
 def test_gradients_of_nothing():
     x, dy = zpm.ZeroPacked(0, 40), torch.empty(0, 30, dtype=BF16, device=DEV)
     db = torch.full((30,), 7.0, device=DEV)

@@ -20,7 +20,7 @@ LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libzero_shard.so")
 SOURCES = ["plan.cpp", "zero_shard_api.cpp", "grads_plan.cpp", "grads_api.cpp", "packed_api.cpp",
            "device.hip",  # kernels.hip, grads.hip
-           "packed_rows.hip", "packed_products.hip"]
+           "packed_rows.hip", "packed_act.hip", "packed_products.hip"]
 HOST_SOURCES = ["offload.cpp"]
 HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -47,12 +47,20 @@ def host_objects(verbose: bool = False, extra_flags=()):
 def build(verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(LIB_DIR, exist_ok=True)
     objs = host_objects(verbose)
-    cmd = ["hipcc", *HIP_FLAGS, *extra_flags, "-shared", "-I", os.path.join(ROOT, "include"), "-I", CSRC,
-           "-o", LIB + ".tmp"]
+    # one process per source, all at once
+    jobs = []
     for s in SOURCES:
-        path = os.path.join(CSRC, s)
-        cmd += (["-x", "hip", path, "-x", "none"] if s.endswith(".cpp") else [path])
-    cmd += [*objs, "-lpthread"]
+        obj = os.path.join(LIB_DIR, s.replace(".", "_") + ".o")
+        cmd = ["hipcc", *HIP_FLAGS, *extra_flags, "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-c", "-x", "hip",
+               os.path.join(CSRC, s), "-o", obj]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        jobs.append((cmd, obj, subprocess.Popen(cmd)))
+    failed = [cmd for cmd, _, job in jobs if job.wait() != 0]
+    if failed:
+        raise subprocess.CalledProcessError(1, failed[0])
+    cmd = ["hipcc", "--offload-arch=gfx950", "-shared", "-fPIC", "-o", LIB + ".tmp", *[obj for _, obj, _ in jobs], *objs,
+           "-lpthread"]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)

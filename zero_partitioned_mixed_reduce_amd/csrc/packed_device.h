@@ -31,11 +31,22 @@ __device__ __forceinline__ void store_any(void* p, V v) {
   __builtin_memcpy(p, &v, sizeof(V));
 }
 
-// Two values rounded to nearest even into a 16-bit format; a NaN becomes the positive quiet one.
+// Makes every NaN among x the positive quiet one, as which a 16-bit destination gets it; one comparison
+// sees two values.
+template <int N>
+__device__ __forceinline__ void one_nan(float (&x)[N]) {
+  static_assert(N % 2 == 0, "pairs");
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < N; i += 2) any |= __builtin_isunordered(x[i], x[i + 1]);
+  if (__builtin_expect(any, 0)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = __builtin_isnan(x[i]) ? __uint_as_float(0x7FC00000u) : x[i];
+  }
+}
+// Two values rounded to nearest even into a 16-bit format.
 template <int DT>
 __device__ __forceinline__ uint32_t enc2(float a, float b) {
-  a = __builtin_isnan(a) ? __uint_as_float(0x7FC00000u) : a;
-  b = __builtin_isnan(b) ? __uint_as_float(0x7FC00000u) : b;
   if constexpr (DT == ZERO_BF16) {
     const f32x2 v = {a, b};
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
@@ -90,17 +101,20 @@ __device__ __forceinline__ uint32_t max_bits(uint32_t m) {
   return __float_as_uint(dec_lo<DT>(a > b ? a : b));
 }
 
-// Elements [c, c + 8) of a row of `cols`; zeros past its end (and before its start, never read).
-template <int DT>
+// Elements [c, c + 8) of a row of `cols`; zeros past its end.  TAIL false: cols is a multiple of 8, and so
+// there are all of them or none (the code for some of them costs the others registers).
+template <int DT, bool TAIL = true>
 __device__ __forceinline__ Raw8<DT> load8(const char* row, int64_t c, int64_t cols) {
   constexpr int S = esize(DT);
   Raw8<DT> r;
   const char* p = row + c * S;
-  if (c + 8 <= cols) {
+  if (TAIL ? c + 8 <= cols : c < cols) {
     r = load_any<Raw8<DT>>(p);
-  } else {
+    return r;
+  }
 #pragma unroll
-    for (int i = 0; i < 2 * S; ++i) r.v[i >> 2][i & 3] = 0;
+  for (int i = 0; i < 2 * S; ++i) r.v[i >> 2][i & 3] = 0;
+  if constexpr (TAIL) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (c + i < cols) {
@@ -110,13 +124,13 @@ __device__ __forceinline__ Raw8<DT> load8(const char* row, int64_t c, int64_t co
   }
   return r;
 }
-// Stores x to elements [c, c + 8) of a row of `cols`, those within it.
-template <int DT>
-__device__ __forceinline__ void store8(char* row, int64_t c, int64_t cols, const float (&x)[8]) {
+// Stores x to elements [c, c + 8) of a row of `cols`, those within it (TAIL false: all are).
+template <int DT, bool TAIL = true>
+__device__ __forceinline__ void store8(char* row, int64_t c, int64_t cols, float (&x)[8]) {
   constexpr int S = esize(DT);
   char* p = row + c * S;
   if constexpr (DT == ZERO_F32) {
-    if (c + 8 <= cols) {
+    if (!TAIL || c + 8 <= cols) {
       store_any(p, f32x4{x[0], x[1], x[2], x[3]});
       store_any(p + 16, f32x4{x[4], x[5], x[6], x[7]});
     } else {
@@ -125,10 +139,11 @@ __device__ __forceinline__ void store8(char* row, int64_t c, int64_t cols, const
         if (c + i < cols) store_any(p + 4 * i, x[i]);
     }
   } else {
+    one_nan(x);
     u32x4 v;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = enc2<DT>(x[2 * i], x[2 * i + 1]);
-    if (c + 8 <= cols) {
+    if (!TAIL || c + 8 <= cols) {
       store_any(p, v);
     } else {
 #pragma unroll
@@ -138,8 +153,24 @@ __device__ __forceinline__ void store8(char* row, int64_t c, int64_t cols, const
   }
 }
 
-// Value b (0 to 3) of four 8-bit integers.
-__device__ __forceinline__ float q_of(uint32_t four, int b) { return (float)(int8_t)(four >> (8 * b)); }
+// Byte B of four 8-bit integers, signed, as a float in one instruction (the compiler takes two).
+template <int B>
+__device__ __forceinline__ float q_of(uint32_t four) {
+  float x = 0.0f;
+#ifdef __HIP_DEVICE_COMPILE__
+  if constexpr (B == 0) asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_0" : "=v"(x) : "v"(four));
+  if constexpr (B == 1) asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1" : "=v"(x) : "v"(four));
+  if constexpr (B == 2) asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2" : "=v"(x) : "v"(four));
+  if constexpr (B == 3) asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3" : "=v"(x) : "v"(four));
+#endif
+  return x;
+}
+__device__ __forceinline__ void values4(uint32_t four, float scale, float* x) {
+  x[0] = q_of<0>(four) * scale;
+  x[1] = q_of<1>(four) * scale;
+  x[2] = q_of<2>(four) * scale;
+  x[3] = q_of<3>(four) * scale;
+}
 
 // How a row is rounded, from the bits of its largest magnitude.
 struct Rounding {

@@ -33,8 +33,9 @@ __device__ __forceinline__ float load1(const MatArg& a, int64_t at) {
 }
 // N consecutive elements of a row, those before column n (N = 4 or 16), at any alignment.
 template <int DT, int N>
-__device__ __forceinline__ void store_run(char* row, int64_t col, int64_t n, const float (&x)[N]) {
+__device__ __forceinline__ void store_run(char* row, int64_t col, int64_t n, float (&x)[N]) {
   constexpr int S = esize(DT);
+  if constexpr (DT != ZERO_F32) one_nan(x);
   char* p = row + col * S;
   uint32_t w[N * S / 4];
 #pragma unroll
@@ -556,18 +557,16 @@ __global__ void __launch_bounds__(WI* WJ * 64, 2) grad_kernel(GradArgs g, uint32
 #pragma unroll
     for (int u = 0; u < LQ; ++u) {
       const int s = q_row(u), c = q_seg(u);
-      // as unsigned bytes q + 128, which take one instruction each: (q + 128) scale - 128 scale, exact
-      const float scale = FEED == kScaled ? 1.0f : h.qs[u], shift = -128.0f * scale;
       asm volatile("" : "+v"(h.q[u]));  // not taken apart before: its bytes in a register each would wait for it
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         u32x2 o;
-        const uint32_t w = h.q[u][k] ^ 0x80808080u;
+        float v[4] = {q_of<0>(h.q[u][k]), q_of<1>(h.q[u][k]), q_of<2>(h.q[u][k]), q_of<3>(h.q[u][k])};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const f32x2 v = {__builtin_fmaf((float)(uint8_t)(w >> (16 * e)), scale, shift),
-                           __builtin_fmaf((float)(uint8_t)(w >> (16 * e + 8)), scale, shift)};
-          o[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+          f32x2 w = {v[2 * e], v[2 * e + 1]};
+          if constexpr (FEED != kScaled) w = f32x2{w.x * h.qs[u], w.y * h.qs[u]};
+          o[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(w, bf16x2));
         }
         *(u32x2*)(lq + s * BJ * 2 + ((((c & ~3) + k) ^ seg_swizzle(s)) << 5) + (c & 3) * 8) = o;
       }
@@ -761,9 +760,13 @@ __global__ void __launch_bounds__(256) columns_join_kernel(const float* part, in
   if (wave != 0 || c >= n) return;
   float v = (lds[0][lane] + lds[1][lane]) + (lds[2][lane] + lds[3][lane]);
   if (accumulate) v += load1(db, c);
-  if (db.dtype == ZERO_F32) ((float*)db.p)[c] = v;
-  else if (db.dtype == ZERO_BF16) ((uint16_t*)db.p)[c] = (uint16_t)enc2<ZERO_BF16>(v, 0.0f);
-  else ((uint16_t*)db.p)[c] = (uint16_t)enc2<ZERO_F16>(v, 0.0f);
+  if (db.dtype == ZERO_F32) {
+    ((float*)db.p)[c] = v;
+    return;
+  }
+  float x[2] = {v, 0.0f};
+  one_nan(x);
+  ((uint16_t*)db.p)[c] = (uint16_t)(db.dtype == ZERO_BF16 ? enc2<ZERO_BF16>(x[0], 0.0f) : enc2<ZERO_F16>(x[0], 0.0f));
 }
 
 }  // namespace packed
