@@ -32,7 +32,9 @@
  *   weight_grad  dw = sum over tokens of dy * x        [n][k]  [+ dw]
  *                db = sum over tokens of dy            [n]     [+ db]
  *   input_grad   dx = sum over channels of dy * w      [m][k]  [+ dx]
- * each rounded once to its result's type, to nearest even.  The gradients' sums
+ * each rounded once to its result's type, to nearest even (fp16 results beyond
+ * 65504 become infinite; a NaN is written to a 16-bit result as the format's
+ * positive canonical quiet NaN).  The gradients' sums
  * are fp32 sums of exact products where dy is bf16 and the rows' scales are
  * powers of two (ZERO_SCALE_POW2); else dy * scale enters as the sum of two bf16
  * values: exact for fp16 dy and powers of two, within 2^-17 of itself for

@@ -76,7 +76,7 @@ typedef enum {
   ZERO_ESTATE = -4  /* call out of the step order                                    */
 } zero_status_t;
 
-typedef enum { ZERO_F16 = 1, ZERO_BF16 = 2, ZERO_F32 = 3 /* zero_grads.h only */ } zero_dtype_t;
+typedef enum { ZERO_F16 = 1, ZERO_BF16 = 2, ZERO_F32 = 3 /* not here: zero_grads.h, zero_packed.h */ } zero_dtype_t;
 
 typedef struct zero_shard* zero_shard_t; /* opaque host handle */
 

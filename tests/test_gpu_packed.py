@@ -228,6 +228,9 @@ def test_linear_without_input_features():
     x.scale.fill_(1), w.scale.fill_(1)
     assert torch.equal(x.zero_packed_linear(w, bias=b, dtype=F32), b.expand(5, 9))
     assert not x.zero_packed_linear(w).any()
+    x = zpm.ZeroPacked(300, 0)
+    x.scale.fill_(1)
+    assert torch.equal(x.zero_packed_linear(w, bias=b, dtype=F32), b.expand(300, 9))
 
 
 def test_linear_far_offsets():

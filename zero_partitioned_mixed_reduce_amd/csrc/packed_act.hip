@@ -181,9 +181,12 @@ __global__ void __launch_bounds__(256) act_grad_kernel(PackArg xp, MatArg dy, Ma
   float d[2][8];
 #pragma unroll
   for (int h = 0; h < 2; ++h) decode8<DY>(load8<DY, TAIL>(src, c + 8 * h, n), d[h]);
+  // all results before the first store, so that the two halves of a line follow each other (written
+  // apart, 12% more went below the L2)
+  float o[2][8], o2[2][8];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    float o[8], o2[8], xa[8], xb[8];
+    float xa[8], xb[8];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       values4(qa[2 * h + i], s, xa + 4 * i);
@@ -194,16 +197,20 @@ __global__ void __launch_bounds__(256) act_grad_kernel(PackArg xp, MatArg dy, Ma
       float f, slope;
       curve<KIND>(xa[i], f, slope);
       if constexpr (GATED) {
-        o[i] = d[h][i] * xb[i] * slope;
-        o2[i] = d[h][i] * f;
+        o[h][i] = d[h][i] * xb[i] * slope;
+        o2[h][i] = d[h][i] * f;
       } else {
-        o[i] = d[h][i] * slope;
+        o[h][i] = d[h][i] * slope;
       }
     }
-    if (c + 8 * h < n) {
-      store8<DX, TAIL>(dst, c + 8 * h, n, o);
-      if constexpr (GATED) store8<DX, TAIL>(dst + n * esize(DX), c + 8 * h, n, o2);
-    }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (c + 8 * h < n) store8<DX, TAIL>(dst, c + 8 * h, n, o[h]);
+  if constexpr (GATED) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (c + 8 * h < n) store8<DX, TAIL>(dst + n * esize(DX), c + 8 * h, n, o2[h]);
   }
 }
 

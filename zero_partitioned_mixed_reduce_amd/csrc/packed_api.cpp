@@ -96,9 +96,9 @@ zero_status_t check_workspace(void* workspace, int64_t capacity, int64_t need, c
   return ZERO_OK;
 }
 
-// A launch has fewer than 2^32 threads, here in blocks of at most 512.
+// A launch has fewer than 2^32 threads, here in blocks of at most 512, two for each tile.
 zero_status_t check_tiles(const zs::ProductPlan& p) {
-  return p.tiles_i * p.tiles_j * p.splits < (int64_t)1 << 23 ? ZERO_OK : bad("a result of more than 2^23 tiles");
+  return p.tiles_i * p.tiles_j * p.splits < (int64_t)1 << 22 ? ZERO_OK : bad("a result of 2^22 tiles or more");
 }
 
 int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }

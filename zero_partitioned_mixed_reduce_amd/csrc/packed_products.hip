@@ -781,10 +781,10 @@ static int64_t join_grid(int64_t quads) {
 
 // Tiles of `bi` x `bj` and a contraction of `steps`: split until the chip's 256 compute units have a
 // block each (of the small tiles two), but no finer than four steps to a split, and not beyond where
-// what the splits write and the join reads takes longer than the steps saved: a step takes about
-// 0.35 us, and a split about 2 ps for each result, so the sum is least at the root of their ratio
-// (128 tokens of 4096 x 4096: 16 splits 30 us, 4 splits 18).
-static ProductPlan plan_product(int64_t ni, int64_t nj, int64_t steps, int64_t bi, int64_t bj, int64_t elem) {
+// what the splits write and the join reads takes longer than the steps saved: a step takes `step_us`
+// and a split about 2 ps for each result, so the sum is least at the root of their ratio (the
+// linear layer of 128 tokens, 4096 x 4096: 16 splits 30 us, 4 splits 18).
+static ProductPlan plan_product(int64_t ni, int64_t nj, int64_t steps, int64_t bi, int64_t bj, double step_us) {
   ProductPlan p{};
   p.tile = (int32_t)bi;
   p.tiles_i = up(ni, bi);
@@ -793,26 +793,27 @@ static ProductPlan plan_product(int64_t ni, int64_t nj, int64_t steps, int64_t b
   const int64_t tiles = p.tiles_i * p.tiles_j;
   int64_t s = tiles > 0 ? (bi == 128 ? 512 : 256) / tiles : 1;  // of the small tiles two at a time
   if (s > steps / 4) s = steps / 4;
-  const int64_t least = (int64_t)std::sqrt(175000.0 * (double)steps / ((double)ni * (double)nj + 1.0));
+  const int64_t least = (int64_t)std::sqrt(step_us * 5e5 * (double)steps / ((double)ni * (double)nj + 1.0));
   if (s > least) s = least;
   if (s < 1) s = 1;
   p.splits = up(steps > 0 ? steps : 1, up(steps > 0 ? steps : 1, s));
-  p.ws_bytes = p.splits > 1 ? p.splits * ni * (up(nj, 4) * 4) * elem : 0;
+  p.ws_bytes = p.splits > 1 ? p.splits * ni * (up(nj, 4) * 4) * 4 : 0;
   return p;
 }
 
 constexpr int64_t kFewTokens = 64;  // the most that linear_few_kernel takes
+constexpr double kBigStep = 0.4, kLinearStep = 0.35, kGradStep = 1.0;  // us of a step of large and of small tiles
 
 ProductPlan plan_linear(int64_t m, int64_t k, int64_t n) {
   if (m <= kFewTokens) {
-    ProductPlan few = plan_product(m, n, 1, kFewTokens, 16, 4);
+    ProductPlan few = plan_product(m, n, 1, kFewTokens, 16, kLinearStep);
     few.tile = 16;
     few.splits = 1;
     few.ws_bytes = 0;
     return few;
   }
-  const ProductPlan p = plan_product(m, n, up(k, kStepK), 256, 256, 4);
-  return p.tiles_i * p.tiles_j >= 256 ? p : plan_product(m, n, up(k, kStepK), 128, 128, 4);
+  const ProductPlan p = plan_product(m, n, up(k, kStepK), 256, 256, kBigStep);
+  return p.tiles_i * p.tiles_j >= 256 ? p : plan_product(m, n, up(k, kStepK), 128, 128, kLinearStep);
 }
 
 // Four waves to 16 channels fill the chip from 8192 channels on; fewer channels take more waves each.
@@ -846,8 +847,8 @@ static bool direct(const GradArgs& g, bool trans) {
          along % 8 == 0 && along > 0 && g.a.pitch <= (int64_t)1 << 22;
 }
 ProductPlan plan_grad(int64_t ni, int64_t nj, int64_t nc) {
-  const ProductPlan p = plan_product(ni, nj, up(nc, kStepS), 256, 256, 4);
-  return p.tiles_i * p.tiles_j >= 128 ? p : plan_product(ni, nj, up(nc, kStepS), 128, 128, 4);
+  const ProductPlan p = plan_product(ni, nj, up(nc, kStepS), 256, 256, kBigStep);
+  return p.tiles_i * p.tiles_j >= 128 ? p : plan_product(ni, nj, up(nc, kStepS), 128, 128, kGradStep);
 }
 
 template <int DT, bool TRANS, int FEED>
