@@ -280,6 +280,36 @@ def test_gradients_to_the_bit(m, k, n, rule, dtype):
     assert torch.equal(old, (dx + 3).float().to(BF16))
 
 
+@pytest.mark.parametrize("dtype, rule", [(BF16, POW2), (F16, POW2), (BF16, MAX)])
+@pytest.mark.parametrize("long", [1, 24, 31, 32, 33, 130, 200, 227, 264, 300])
+def test_gradients_in_large_tiles(long, dtype, rule):
+    """Results of so many tiles that they are the large ones, with ragged edges, and sums that end anywhere in a step:
+    lengths and widths that are multiples of eight and that are not (loaded straight into LDS, and through registers)."""
+    one = lambda rows, seed: torch.exp2(torch.randint(-1, 2, (rows,), generator=gen(seed), device=DEV).float())
+    for k, wide in ((2856, 3080), (2851, 3077)):
+        x, dy = random_packed(long, k, 1, rule, one(long, 6)), whole_dy(long, wide, dtype, 5)
+        assert torch.equal(x.zero_packed_weight_grad(dy, dtype=BF16), (dy.double().T @ values(x)).to(BF16))
+        old = torch.full((wide, k), 3.0, device=DEV)
+        x.zero_packed_weight_grad(dy, out=old, accumulate=True)
+        assert torch.equal(old, (dy.double().T @ values(x) + 3).float())
+        w, dz = random_packed(long, k, 2, rule, one(long, 7)), whole_dy(wide, long, dtype, 8)
+        assert torch.equal(w.zero_packed_input_grad(dz, dtype=F32), (dz.double() @ values(w)).float())
+        v, _ = strided(dz, 8)                           # NaN behind each row
+        assert torch.equal(w.zero_packed_input_grad(v, dtype=F32), (dz.double() @ values(w)).float())
+        v, _ = strided(dy, 8)
+        assert torch.equal(x.zero_packed_weight_grad(v), (dy.double().T @ values(x)).float())
+
+
+@pytest.mark.parametrize("k", [1, 16, 48, 63, 64, 65, 130, 256, 300, 333])
+def test_linear_in_large_tiles(k):
+    x, w = random_packed(4100, k, 1), random_packed(4150, k, 2, MAX, torch.rand(4150, generator=gen(3), device=DEV) + 0.01)
+    y = x.zero_packed_linear(w, bias=w.scale, dtype=F32)
+    assert same_bits(y, linear_expected(x, w, w.scale, F32))
+    out, big = strided(torch.zeros(4100, 4150, dtype=BF16, device=DEV), 7, 1)
+    x.zero_packed_linear(w, out=out)
+    assert torch.equal(out, linear_expected(x, w, None, BF16)) and around(out, big, 1).isnan().all()
+
+
 @pytest.mark.parametrize("rule, dtype", [(POW2, BF16), (POW2, F16), (MAX, BF16), (MAX, F16)])
 @pytest.mark.parametrize("m, k, n", [(40, 50, 60), (1003, 333, 143), (2048, 256, 688), (70, 640, 1600)])
 def test_gradients(m, k, n, rule, dtype):
