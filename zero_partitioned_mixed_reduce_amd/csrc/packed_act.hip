@@ -1,9 +1,9 @@
 // gfx950 kernels of the activation functions: forward, packing the input and the result, and backward
 // from the packed input.  Each element is read and written once; the forward's rows stay in
 // registers while their scales are found, as in packed_rows.hip (rows beyond 16384 elements are
-// read twice).  8192 x 2 x 11008 in bf16, gated, both packed: 165 to 185 us (3.4 to 3.8 TB/s), backward
-// about 135 (5.3).  The forward is bound by its instructions, some 50 an element with an exponential
-// and a reciprocal among them, which wait for the row's scales together.
+// read twice).  8192 x 2 x 11008 in bf16, gated, both packed: 117 to 134 us (4.7 to 5.4 TB/s), backward
+// 135 to 138 (5.2).  The forward has some 50 instructions an element, an exponential and a
+// reciprocal among them, about as long as its bytes take.
 #include "packed_rows.h"
 
 namespace zs {
@@ -216,8 +216,10 @@ __global__ void __launch_bounds__(256) act_grad_kernel(PackArg xp, MatArg dy, Ma
   }
 }
 
-// Calls fn with TAIL, T and U of rows of `cols` elements.  At most two groups of eight a thread: the results
-// stay beside them, and with three or four a block takes a compute unit's registers by itself.
+// Calls fn with TAIL, T and U of rows of `cols` elements.  Two blocks or more have to fit a compute unit, so
+// that one loads while the other computes: 11008 elements gated take 134 us (117 at best) with 512
+// threads of three groups, 185 with 768 of two, of which only one block fits.  Four groups a thread
+// spill registers: the results stay beside them.
 template <class F>
 static void by_length(int64_t cols, F fn) {
   const int64_t groups = (cols + 15) / 16 * 2;
@@ -229,7 +231,7 @@ static void by_length(int64_t cols, F fn) {
     else if (groups <= 256) fn(tail, integral_constant<int, 256>(), integral_constant<int, 1>());
     else if (groups <= 512) fn(tail, integral_constant<int, 256>(), integral_constant<int, 2>());
     else if (groups <= 1024) fn(tail, integral_constant<int, 512>(), integral_constant<int, 2>());
-    else if (groups <= 1536) fn(tail, integral_constant<int, 768>(), integral_constant<int, 2>());
+    else if (groups <= 1536) fn(tail, integral_constant<int, 512>(), integral_constant<int, 3>());
     else if (groups <= 2048) fn(tail, integral_constant<int, 1024>(), integral_constant<int, 2>());
     else fn(tail, integral_constant<int, 1024>(), integral_constant<int, 0>());
   } else {

@@ -43,7 +43,9 @@ class ZeroPacked:
     Tensors given to the calls are matrices on the same GPU whose rows are consecutive elements, at any pitch; what a
     call writes must not overlap what it reads.  Calls use the current stream of that GPU, allocate results (unless out is
     given) and workspaces there, and write behind autograd's back, as into detached tensors.  As with any torch call,
-    tensors used on another stream than the one they were allocated on must be kept until that stream is done with them."""
+    tensors used on another stream than the one they were allocated on must be kept until that stream is done with them,
+    and tensors and packed rows used in a captured graph until its last replay is done.  Two calls that run at the same
+    time must not write the same rows."""
 
     def __init__(self, rows, cols, rule=abi.ZERO_SCALE_POW2, device="cuda"):
         if rows < 0 or cols < 0:
