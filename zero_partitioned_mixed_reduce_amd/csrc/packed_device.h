@@ -102,14 +102,21 @@ __device__ __forceinline__ uint32_t max_bits(uint32_t m) {
 }
 
 // Elements [c, c + 8) of a row of `cols`; zeros past its end.  TAIL false: cols is a multiple of 8, and so
-// there are all of them or none (the code for some of them costs the others registers).
-template <int DT, bool TAIL = true>
+// there are all of them or none (the code for some of them costs the others registers).  ONCE: read past
+// the caches' order of use, by who reads them only once.
+template <int DT, bool TAIL = true, bool ONCE = false>
 __device__ __forceinline__ Raw8<DT> load8(const char* row, int64_t c, int64_t cols) {
   constexpr int S = esize(DT);
   Raw8<DT> r;
   const char* p = row + c * S;
   if (TAIL ? c + 8 <= cols : c < cols) {
-    r = load_any<Raw8<DT>>(p);
+    if constexpr (ONCE) {
+      typedef uint32_t any4 __attribute__((ext_vector_type(4), aligned(2)));
+#pragma unroll
+      for (int i = 0; i < S / 2; ++i) r.v[i] = __builtin_nontemporal_load((const any4*)(p + 16 * i));
+    } else {
+      r = load_any<Raw8<DT>>(p);
+    }
     return r;
   }
 #pragma unroll

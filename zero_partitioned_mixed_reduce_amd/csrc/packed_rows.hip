@@ -4,8 +4,8 @@
 // it in registers between the two, eight elements (16 bytes of 16-bit data) to a load: one wave
 // takes a row of up to 2048 elements, four rows to a block, and a block of 256 to 1024 threads one
 // of up to 32 elements a thread.  Rows beyond 32768 elements are read twice, the second time
-// mostly from the L2 cache.  16384 x 11008 in bf16: packed in 104 to 110 us (4.9 to 5.2 TB/s), read
-// back in 92 to 96 (5.6 to 5.9); a copy reaches 6.4.
+// mostly from the L2 cache.  16384 x 11008 in bf16: packed in 86 us (6.3 TB/s; 110 with ordinary
+// loads), read back in 108 (5.0); a copy reaches 6.4.
 #include "packed_rows.h"
 
 namespace zs {
@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(kRowBlock<T>) write_kernel(MatArg x, PackArg p
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t c = 8 * (int64_t)(t + u * T);
-        raw[u] = load8<DT, TAIL>(src, c, cols);
+        raw[u] = load8<DT, TAIL, true>(src, c, cols);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) m = max_raw<DT>(raw[u], m);
