@@ -379,6 +379,79 @@ def test_gradients_of_extreme_scales(e):
     assert torch.equal(w.zero_packed_input_grad(dz, dtype=F32).double(), dz.double() @ values(w))
 
 
+@pytest.mark.parametrize("m", [45, 48, 300])
+@pytest.mark.parametrize("rule, dtype", [(POW2, BF16), (POW2, F16), (MAX, BF16), (MAX, F16)])
+@pytest.mark.parametrize("e", [-126, -119, -100, 100, 121])
+def test_gradients_at_the_ends_of_the_range(e, rule, dtype, m):
+    """Scales at both ends, dy from the type's usual smallest to beyond what dy * scale could hold: products that are
+    multiples of 2^-149 are exact, and columns of zeros are zeros wherever dy is finite."""
+    k = 72
+    x = random_packed(m, k, 1, rule, torch.full((m,), 2.0 ** e, device=DEV))
+    x._q[:, 5], x._q[:, 64] = 0, 0
+    for d in (-24, -14, -3) if e < 0 else (-24, -20):
+        for wide in (33, 40):                           # through registers, and bf16 with powers of two straight into LDS
+            unit = max(e + d, -149)
+            dy = whole_dy(m, wide, dtype, 5, 15) * 2.0 ** (unit - e)
+            got = x.zero_packed_weight_grad(dy)
+            assert torch.equal(got.double(), dy.double().T @ values(x)) and got.any()
+            dz = whole_dy(wide, m, dtype, 6, 15) * 2.0 ** (unit - e)
+            assert torch.equal(x.zero_packed_input_grad(dz, dtype=F32).double(), dz.double() @ values(x))
+    x._q.abs_().clamp_(max=63)
+    for dy in (torch.full((m, 40), 6e4, device=DEV).to(dtype), torch.full((m, 33), 2.0 ** 15, device=DEV).to(dtype)):
+        for got, want in ((x.zero_packed_weight_grad(dy), (dy.double().T @ values(x)).float()),
+                          (x.zero_packed_input_grad(dy.T.contiguous(), dtype=F32), (dy.double().T @ values(x)).float())):
+            assert not got[:, 5].any() and not got[:, 64].any() and not got.isnan().any()
+            # all terms but second ones are positive, fp16 dy has two: each addition is off by half a step of the sum
+            assert torch.equal(got.isinf(), want.isinf()) and (e > 0 or ((got - want).abs() <= want * (2 * m + 16) * 2.0 ** -24).all())
+
+
+@pytest.mark.parametrize("m", [45, 48, 300])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("e", [-126, -100, 0, 120])
+def test_gradients_by_the_maximum_at_the_ends_of_the_range(e, dtype, m):
+    """Scales that are no powers of two: dy times a scale's significand is off by 2^-17 of itself (2^-24 more for its product
+    in fp32), whatever the scale's exponent."""
+    x = random_packed(m, 72, 1, MAX, (1 + torch.rand(m, generator=gen(2), device=DEV)) * 2.0 ** e)
+    x._q[:, 5] = 0
+    small = 2.0 ** -20 if e > 0 else 2.0 ** -3          # dy of at most 4 to 5 times this: finite sums
+    dy = (torch.randn(m, 40, generator=gen(3), device=DEV) * small).to(dtype)
+    a, v = dy.double().T, values(x)
+    want, mag = a @ v, a.abs() @ v.abs()
+    # two terms a product; a sum below the normal numbers is off by half of 2^-149 an addition
+    most = mag * ((2 * m + 16) * 2.0 ** -24 + 2.0 ** -17 + 2.0 ** -24) + (2 * m + 16) * 2.0 ** -150
+    for got in (x.zero_packed_weight_grad(dy), x.zero_packed_input_grad(dy.T.contiguous(), dtype=F32)):
+        assert ((got.double() - want).abs() <= most).all() and not got[:, 5].any()
+    # dy beyond what dy * scale could hold
+    dy.fill_(6e4)
+    got = x.zero_packed_weight_grad(dy)
+    assert not got[:, 5].any() and (e < 0 or torch.equal(got.isfinite(), (dy.double().T @ v).float().isfinite()))
+    x.scale[7] = math.nan
+    assert x.zero_packed_weight_grad(dy).isnan().all() and x.zero_packed_input_grad(dy.T.contiguous()).isnan().all()
+
+
+@pytest.mark.parametrize("m", [45, 300])
+@pytest.mark.parametrize("rule", [POW2, MAX])
+def test_gradients_of_rows_of_all_scales(rule, m):
+    """Rows next to each other whose scales lie hundreds of binades apart, and dy the other way round: products are whole
+    numbers, and so every sum is exact.  Then the smallest rows by themselves, whose sums no other row joins."""
+    g = gen(m)
+    e = torch.randint(-94, 84, (m,), generator=g, device=DEV).float()
+    e[:8] = torch.tensor([-94, -33, -32, -31, 31, 32, 33, 84], device=DEV)
+    x = random_packed(m, 72, 1, rule, torch.exp2(e))
+    dy = (whole_dy(m, 40, BF16, 5).float() * torch.exp2(-e)[:, None]).to(BF16)
+    want = dy.double().T @ values(x)
+    assert torch.equal(x.zero_packed_weight_grad(dy).double(), want)
+    assert torch.equal(x.zero_packed_input_grad(dy.T.contiguous(), dtype=F32).double(), want)
+    small = e < -32
+    x._q[~small, :9] = 0
+    for dtype in (BF16, F16):
+        dz = whole_dy(m, 40, dtype, 6)
+        want = dz.double().T @ values(x)
+        most = (dz.double().abs().T @ values(x).abs()) * (2 * m + 16) * 2.0 ** -24
+        for got in (x.zero_packed_weight_grad(dz), x.zero_packed_input_grad(dz.T.contiguous(), dtype=F32)):
+            assert ((got.double() - want).abs() <= most).all() and got[:, :9].abs().max() < 2.0 ** -15
+
+
 def test_gradients_of_nothing():
     x, dy = zpm.ZeroPacked(0, 40), torch.empty(0, 30, dtype=BF16, device=DEV)
     db = torch.full((30,), 7.0, device=DEV)

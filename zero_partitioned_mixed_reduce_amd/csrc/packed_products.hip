@@ -374,21 +374,39 @@ constexpr int kStepS = 32;  // s of a tile step: one matrix instruction's
 enum Feed : int {
   kDirect = 0,  // bf16 as it is, loaded into LDS: rows and columns on 16-byte boundaries
   kPlain = 1,   // bf16 as it is, through registers, at any alignment
-  kScaled = 2,  // times the scales, as two bf16 terms, through registers
+  kTerms = 2,   // fp16 as two bf16 terms, through registers
+  kScaled = 3,  // times the scales (see Factors), as two bf16 terms, through registers
 };
+
+// A scale that is no power of two does not fit into a bf16 value beside q: a is multiplied by it.  Outside
+// [2^-32, 2^32) only by its significand, in [1, 2), and q by the power of two that is left, exactly, so that
+// neither leaves its type's range at either end of the scales'.  A step with none of these leaves q
+// alone: q multiplied in every step takes 7% longer (8192 x 4096 x 11008: 1920 for 1760 us).
+struct Factors {
+  float a, q;
+};
+__device__ __forceinline__ bool ordinary(float scale) { return __float_as_uint(scale) - 0x2F800000u < 0x20000000u; }
+__device__ __forceinline__ Factors factors(float scale) {
+  if (ordinary(scale)) return {scale, 1.0f};
+  const uint32_t b = __float_as_uint(scale);
+  const float power = __uint_as_float(b & 0xFF800000u);
+  return {__uint_as_float((b & 0x007FFFFFu) | 0x3F800000u), __builtin_isnan(scale) ? scale : power};
+}
 
 // Place of 16-element segment g of row s in a tile [s][...] is g ^ this: the rows that a transposing
 // read takes together lie in different banks.
 __device__ __forceinline__ int seg_swizzle(int s) { return (s & 3) | ((s >> 1) & 4); }
 
-// Splits two values into two bf16 values each whose sum is theirs to 16 bits (exactly, if they have
-// no more).
+// Splits two values into two bf16 values each whose sum is theirs to 16 bits: exactly fp16's eleven, and
+// within 2^-17 of itself a product with a scale.  A third term would bring that to the product's own
+// 2^-24, for half as many matrix instructions again; 16-bit results would not show it.
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
   hi = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
-  const float ha = dec_lo<ZERO_BF16>(hi), hb = dec_hi<ZERO_BF16>(hi);
-  // nothing is left of an infinity
-  const float ra = __builtin_isinf(ha) ? 0.0f : a - ha, rb = __builtin_isinf(hb) ? 0.0f : b - hb;
-  lo = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{ra, rb}), bf16x2));
+  // what is left of an infinity is one of its sign
+  constexpr float kMost = 0x1.fffffep127f;
+  const float ha = __builtin_amdgcn_fmed3f(dec_lo<ZERO_BF16>(hi), -kMost, kMost);
+  const float hb = __builtin_amdgcn_fmed3f(dec_hi<ZERO_BF16>(hi), -kMost, kMost);
+  lo = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a - ha, b - hb}), bf16x2));
 }
 
 // A block makes a tile of BI x BJ results with WI x WJ waves: 256 x 256 with eight, or 128 x 256 where a
@@ -405,7 +423,7 @@ __global__ void __launch_bounds__(WI* WJ * 64, 2) grad_kernel(GradArgs g, uint32
   constexpr int W = WI * WJ, T = W * 64, S = kStepS;
   constexpr int TI = BI / WI / 16, TJ = BJ / WJ / 16;
   constexpr int LA = BI * S / 8 / T, LQ = BJ * S / 16 / T;  // 16-byte chunks of a thread
-  constexpr int TERMS = FEED == kScaled ? 2 : 1;
+  constexpr int TERMS = FEED == kTerms || FEED == kScaled ? 2 : 1;
   constexpr int ABYTES = BI * S * 2;
   constexpr int kStages = FEED == kDirect ? 4 : 2;  // tile steps in LDS
   static_assert(BI * S / 8 % T == 0 && BJ * S / 16 % T == 0, "whole chunks");
@@ -474,6 +492,7 @@ __global__ void __launch_bounds__(WI* WJ * 64, 2) grad_kernel(GradArgs g, uint32
   struct Held {
     Raw8<ZERO_BF16> a[FEED == kDirect ? 1 : LA];
     float as[FEED == kScaled ? (TRANS ? LA : LA * 8) : 1];
+    float row;  // kScaled: the scale of row lane % 32 of the step
     u32x4 q[LQ];
     float qs[LQ];
   } held[2];
@@ -518,6 +537,7 @@ __global__ void __launch_bounds__(WI* WJ * 64, 2) grad_kernel(GradArgs g, uint32
     }
     const char* base = (const char*)g.q.q + s0 * g.q.pitch + j0;
     const float* scale = g.q.scale + s0;
+    if constexpr (FEED == kScaled) h.row = scale[(lane & (S - 1)) < left ? lane & (S - 1) : left - 1];
 #pragma unroll
     for (int u = 0; u < LQ; ++u) {
       const int r = q_row(u);
@@ -535,6 +555,14 @@ __global__ void __launch_bounds__(WI* WJ * 64, 2) grad_kernel(GradArgs g, uint32
   const auto stage = [&](auto k, Held& h) __attribute__((always_inline)) {
     [[maybe_unused]] char* la = a_place(k);
     char* lq = q_place(k);
+    [[maybe_unused]] bool split = false;  // the same for all threads of the block
+    if constexpr (FEED == kScaled) {
+      split = __builtin_amdgcn_ballot_w64(!ordinary(h.row)) != 0;
+      if (split) {
+#pragma unroll
+        for (float& s : h.as) s = factors(s).a;
+      }
+    }
     if constexpr (FEED != kDirect) {
 #pragma unroll
       for (int u = 0; u < LA; ++u) {
@@ -547,13 +575,17 @@ __global__ void __launch_bounds__(WI* WJ * 64, 2) grad_kernel(GradArgs g, uint32
           const int i = id / (S / 8), c = id % (S / 8);
           to = i * S * 2 + ((c ^ (-(i >> 2) & 3)) << 4);
         }
-        if constexpr (FEED == kScaled) {
+        if constexpr (TERMS == 2) {
           u32x4 hi, lo;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float s0 = h.as[TRANS ? u : u * 8 + 2 * k], s1 = h.as[TRANS ? u : u * 8 + 2 * k + 1];
+            float a = dec_lo<DT>(h.a[u].v[0][k]), b = dec_hi<DT>(h.a[u].v[0][k]);
+            if constexpr (FEED == kScaled) {  // with an addend the conversion from fp16 is part of the instruction
+              a = __builtin_fmaf(a, h.as[TRANS ? u : u * 8 + 2 * k], 0.0f);
+              b = __builtin_fmaf(b, h.as[TRANS ? u : u * 8 + 2 * k + 1], 0.0f);
+            }
             uint32_t x, y;
-            split2(dec_lo<DT>(h.a[u].v[0][k]) * s0, dec_hi<DT>(h.a[u].v[0][k]) * s1, x, y);
+            split2(a, b, x, y);
             hi[k] = x;
             lo[k] = y;
           }
@@ -570,18 +602,26 @@ __global__ void __launch_bounds__(WI* WJ * 64, 2) grad_kernel(GradArgs g, uint32
 #pragma unroll
     for (int u = 0; u < LQ; ++u) {
       const int s = q_row(u), c = q_seg(u);
-      asm volatile("" : "+v"(h.q[u]));  // not taken apart before: its bytes in a register each would wait for it
+      const auto put = [&](auto scaled, float qs) __attribute__((always_inline)) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        u32x2 o;
-        float v[4] = {q_of<0>(h.q[u][k]), q_of<1>(h.q[u][k]), q_of<2>(h.q[u][k]), q_of<3>(h.q[u][k])};
+        for (int k = 0; k < 4; ++k) {
+          u32x2 o;
+          float v[4] = {q_of<0>(h.q[u][k]), q_of<1>(h.q[u][k]), q_of<2>(h.q[u][k]), q_of<3>(h.q[u][k])};
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          f32x2 w = {v[2 * e], v[2 * e + 1]};
-          if constexpr (FEED != kScaled) w = f32x2{w.x * h.qs[u], w.y * h.qs[u]};
-          o[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(w, bf16x2));
+          for (int e = 0; e < 2; ++e) {
+            f32x2 w = {v[2 * e], v[2 * e + 1]};
+            if constexpr (decltype(scaled)::value) w = f32x2{w.x * qs, w.y * qs};
+            o[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(w, bf16x2));
+          }
+          *(u32x2*)(lq + s * BJ * 2 + ((((c & ~3) + k) ^ seg_swizzle(s)) << 5) + (c & 3) * 8) = o;
         }
-        *(u32x2*)(lq + s * BJ * 2 + ((((c & ~3) + k) ^ seg_swizzle(s)) << 5) + (c & 3) * 8) = o;
+      };
+      asm volatile("" : "+v"(h.q[u]));  // not taken apart before: its bytes in a register each would wait for it
+      if constexpr (FEED == kScaled) {
+        if (split) put(std::true_type(), factors(__shfl(h.row, s)).q);
+        else put(std::false_type(), 1.0f);
+      } else {
+        put(std::true_type(), h.qs[u]);
       }
     }
   };
@@ -881,7 +921,9 @@ static void launch_grad_typed(const GradArgs& g, const ProductPlan& p, hipStream
 }
 
 hipError_t launch_grad(const GradArgs& g, bool trans, const ProductPlan& p, hipStream_t st) {
-  if (g.a.dtype == ZERO_F16) {
+  if (g.a.dtype == ZERO_F16 && g.q.rule == ZERO_SCALE_POW2) {
+    trans ? launch_grad_typed<ZERO_F16, true, kTerms>(g, p, st) : launch_grad_typed<ZERO_F16, false, kTerms>(g, p, st);
+  } else if (g.a.dtype == ZERO_F16) {
     trans ? launch_grad_typed<ZERO_F16, true, kScaled>(g, p, st) : launch_grad_typed<ZERO_F16, false, kScaled>(g, p, st);
   } else if (g.q.rule != ZERO_SCALE_POW2) {
     trans ? launch_grad_typed<ZERO_BF16, true, kScaled>(g, p, st) : launch_grad_typed<ZERO_BF16, false, kScaled>(g, p, st);
