@@ -10,7 +10,8 @@ import oracle
 import zero_partitioned_mixed_reduce_amd as zpm
 from tests.gpu_harness import dev16
 from tests.test_gpu_packed import BF16, DEV, F16, F32, GELU, POW2, SILU, f64, gen, packed_of, random_packed, values, whole_dy
-from zero_partitioned_mixed_reduce_amd import ZeroGrads, ZeroPacked
+from zero_partitioned_mixed_reduce_amd import ZeroGrads, ZeroPacked, _abi
+from zero_partitioned_mixed_reduce_amd.packed import matrix
 
 pytestmark = pytest.mark.gpu
 
@@ -270,3 +271,28 @@ def test_leaves_of_an_autograd_graph():
         assert torch.equal(dw, want) and torch.equal(dx, want_x)
     loss.backward()
     assert w.grad.isfinite().all()
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("rows", [1, 9, 700])
+def test_act_without_columns(rows, gated):
+    """Packed results without columns, whose q may be NULL, get the scales of rows of zeros, as zero_packed_write gives them."""
+    stream = torch.cuda.current_stream().cuda_stream
+    x = _abi.zero_matrix_t(None, rows, 0, 0, _abi.ZERO_BF16)
+    sx, sy, sw = (torch.full((rows,), math.nan, device=DEV) for _ in range(3))
+    none = lambda s: _abi.zero_packed_t(None, s.data_ptr(), rows, 0, 16, POW2)
+    zpm.zero_packed_write(x, none(sw), stream)
+    zpm.zero_packed_act(SILU, gated, x, none(sx), None, none(sy), stream)
+    assert not sw.any() and not sx.any() and not sy.any()
+    sx.fill_(math.nan)
+    zpm.zero_packed_act(GELU, gated, x, none(sx), x, None, stream)
+    assert not sx.any()
+    sy.fill_(math.nan)
+    zpm.zero_packed_act(GELU, gated, x, None, None, none(sy), stream)
+    assert not sy.any()
+    # and what follows is the bias, not NaN
+    w, b = ZeroPacked(6, 0), torch.arange(6, device=DEV, dtype=F32)
+    w.scale.fill_(1)
+    y = torch.empty(rows, 6, device=DEV)
+    zpm.zero_packed_linear(none(sy), w._desc, matrix(b, "b"), matrix(y, "y"), None, 0, stream)
+    assert torch.equal(y, b.expand(rows, 6))

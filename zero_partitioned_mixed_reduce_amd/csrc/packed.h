@@ -65,7 +65,7 @@ hipError_t launch_columns(const MatArg& dy, int64_t m, int64_t n, const MatArg& 
 
 hipError_t launch_write(const MatArg& x, const PackArg& p, int64_t rows, int64_t cols, hipStream_t st);
 hipError_t launch_read(const PackArg& p, const MatArg& out, int64_t rows, int64_t cols, hipStream_t st);
-// xp.q, y.p and yp.q may be null
+// xp.scale, y.p and yp.scale may be null: not asked for (a q without columns may be null as well)
 hipError_t launch_act(int kind, bool gated, const MatArg& x, const PackArg& xp, const MatArg& y, const PackArg& yp,
                       int64_t m, int64_t n, hipStream_t st);
 hipError_t launch_act_grad(int kind, bool gated, const PackArg& xp, const MatArg& dy, const MatArg& dx, int64_t m,

@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kRowBlock<T>, 4) act_kernel(MatArg x, PackArg 
       }
     };
     const auto first = [&](int u) __attribute__((always_inline)) {
-      if (yp.q) my = max8(vy[u], my);
+      if (yp.scale) my = max8(vy[u], my);
       mx = max_raw<DT>(a[u], mx);
       if constexpr (GATED) mx = max_raw<DT>(b[u], mx);
     };
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kRowBlock<T>, 4) act_kernel(MatArg x, PackArg 
         compute(u);
         first(u);
       }
-    } else if (xp.q || yp.q) {
+    } else if (xp.scale || yp.scale) {
       for (int64_t c = 8 * t; c < n; c += 8 * T) {
         fetch(0, c);
         compute(0);
@@ -101,10 +101,10 @@ __global__ void __launch_bounds__(kRowBlock<T>, 4) act_kernel(MatArg x, PackArg 
     }
     mx = max_bits<DT>(mx);
     Rounding kx{}, ky{};
-    if (xp.q) kx = xp.rule == ZERO_SCALE_POW2 ? rounding<ZERO_SCALE_POW2>(row_max<T>(mx, lds))
-                                              : rounding<ZERO_SCALE_MAX>(row_max<T>(mx, lds));
-    if (yp.q) ky = yp.rule == ZERO_SCALE_POW2 ? rounding<ZERO_SCALE_POW2>(row_max<T>(my, lds))
-                                              : rounding<ZERO_SCALE_MAX>(row_max<T>(my, lds));
+    if (xp.scale) kx = xp.rule == ZERO_SCALE_POW2 ? rounding<ZERO_SCALE_POW2>(row_max<T>(mx, lds))
+                                                  : rounding<ZERO_SCALE_MAX>(row_max<T>(mx, lds));
+    if (yp.scale) ky = yp.rule == ZERO_SCALE_POW2 ? rounding<ZERO_SCALE_POW2>(row_max<T>(my, lds))
+                                                  : rounding<ZERO_SCALE_MAX>(row_max<T>(my, lds));
     int8_t* qx = xp.q + r * xp.pitch;
     int8_t* qy = yp.q + r * yp.pitch;
     const auto put = [&](const float (&v)[8], const Rounding& k, int32_t rule) __attribute__((always_inline)) {
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kRowBlock<T>, 4) act_kernel(MatArg x, PackArg 
     };
     const auto second = [&](int u, int64_t c) __attribute__((always_inline)) {
       if (c < n && y.p) store_y<TAIL>(y, r, c, n, vy[u]);
-      if (xp.q) {
+      if (xp.scale) {
         float v[8];
         decode8<DT>(a[u], v);
         const u32x2 wa = put(v, kx, xp.rule);
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kRowBlock<T>, 4) act_kernel(MatArg x, PackArg 
           }
         }
       }
-      if (yp.q && c < wide) *(u32x2*)(qy + c) = put(vy[u], ky, yp.rule);
+      if (yp.scale && c < wide) *(u32x2*)(qy + c) = put(vy[u], ky, yp.rule);
     };
     if constexpr (U > 0) {
 #pragma unroll
@@ -146,11 +146,11 @@ __global__ void __launch_bounds__(kRowBlock<T>, 4) act_kernel(MatArg x, PackArg 
       }
     }
     if (t == 0) {
-      if (xp.q) xp.scale[r] = kx.scale;
-      if (yp.q) yp.scale[r] = ky.scale;
+      if (xp.scale) xp.scale[r] = kx.scale;
+      if (yp.scale) yp.scale[r] = ky.scale;
     }
     // the zeros behind a gated row
-    if (GATED && xp.q && xcols + t < padded(xcols)) qx[xcols + t] = 0;
+    if (GATED && xp.scale && xcols + t < padded(xcols)) qx[xcols + t] = 0;
   }
 }
 
