@@ -310,6 +310,59 @@ def test_linear_in_large_tiles(k):
     assert torch.equal(out, linear_expected(x, w, None, BF16)) and around(out, big, 1).isnan().all()
 
 
+ALL_FEEDS = [(BF16, POW2), (F16, POW2), (BF16, MAX), (F16, MAX)]
+
+
+def halves(rows, seed):
+    """Scales a half, one and two."""
+    return torch.exp2(torch.randint(-1, 2, (rows,), generator=gen(seed), device=DEV).float())
+
+
+@pytest.mark.parametrize("dtype, rule", ALL_FEEDS)
+@pytest.mark.parametrize("long", [2050, 4093, 4104])
+def test_gradients_of_long_sums_in_large_tiles(long, dtype, rule):
+    """Dense sums of up to 129 steps of large tiles, not split: the steps' places in LDS go round many times."""
+    for k, wide in ((2856, 3080), (2851, 3077)):
+        assert zpm.zero_packed_workspace(zpm.ZERO_PACKED_INPUT_GRAD, wide, k, long) == 0
+        assert long * 3 * 127 * 4 < 2 ** 24             # in units of half a step: every sum is exact
+        x, dy = random_packed(long, k, 1, rule, halves(long, 6)), whole_dy(long, wide, dtype, 5)
+        assert torch.equal(x.zero_packed_weight_grad(dy), (dy.double().T @ values(x)).float())
+        dz = whole_dy(wide, long, dtype, 8)
+        assert torch.equal(x.zero_packed_input_grad(dz, dtype=F32), (dz.double() @ values(x)).float())
+
+
+@pytest.mark.parametrize("dtype, rule", ALL_FEEDS)
+@pytest.mark.parametrize("long", [5401, 8192])
+@pytest.mark.parametrize("wide, k", [(2048, 4096), (4096, 2048), (2041, 4090)])
+def test_gradients_of_split_sums_in_large_tiles(wide, k, long, dtype, rule):
+    """Results of exactly 128 large tiles, half of what the chip takes at once: long sums are split and joined."""
+    call = zpm.zero_packed_workspace
+    assert call(zpm.ZERO_PACKED_INPUT_GRAD, wide, k, long) == (2 * wide * ((k + 3) // 4 * 4) * 4 + 255) // 256 * 256
+    assert long * 3 * 127 * 4 < 2 ** 24
+    x, dy, db = random_packed(long, k, 1, rule, halves(long, 6)), whole_dy(long, wide, dtype, 5), torch.empty(wide, device=DEV)
+    want = dy.double().T @ values(x)
+    assert torch.equal(x.zero_packed_weight_grad(dy, bias_grad=db), want.float())
+    assert torch.equal(db, dy.double().sum(0).float())
+    old, big = strided(torch.full((wide, k), 3.0, device=DEV), 5, 3)
+    x.zero_packed_weight_grad(dy, out=old, accumulate=True)
+    assert torch.equal(old, (want + 3).float()) and around(old, big, 3).isnan().all()
+    assert torch.equal(x.zero_packed_weight_grad(dy, dtype=BF16), want.to(BF16))
+    dz = whole_dy(wide, long, dtype, 8)
+    want = dz.double() @ values(x)
+    assert torch.equal(x.zero_packed_input_grad(dz, dtype=F32), want.float())
+    old = torch.full((wide, k), 3.0, device=DEV, dtype=BF16)
+    x.zero_packed_input_grad(dz, out=old, accumulate=True)
+    assert torch.equal(old, (want + 3).float().to(BF16))
+
+
+@pytest.mark.parametrize("k", [4096, 4091, 1040])
+def test_linear_of_long_sums_in_large_tiles(k):
+    x, w = random_packed(4100, k, 1), random_packed(4150, k, 2, MAX, torch.rand(4150, generator=gen(3), device=DEV) + 0.01)
+    assert zpm.zero_packed_workspace(zpm.ZERO_PACKED_LINEAR, 4100, k, 4150) == 0
+    assert same_bits(x.zero_packed_linear(w, bias=w.scale, dtype=F32), linear_expected(x, w, w.scale, F32))
+    assert torch.equal(x.zero_packed_linear(w), linear_expected(x, w, None, BF16))
+
+
 @pytest.mark.parametrize("rule, dtype", [(POW2, BF16), (POW2, F16), (MAX, BF16), (MAX, F16)])
 @pytest.mark.parametrize("m, k, n", [(40, 50, 60), (1003, 333, 143), (2048, 256, 688), (70, 640, 1600)])
 def test_gradients(m, k, n, rule, dtype):
