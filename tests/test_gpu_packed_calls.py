@@ -186,6 +186,52 @@ def test_split_products_in_graphs_and_on_streams():
         assert torch.equal(a, want) and torch.equal(b, want_y)
 
 
+def test_split_linear_and_column_sums_in_graphs_and_on_streams():
+    """A linear layer of so many tokens that its sums are split and joined, and a weight gradient whose bias gradient is
+    joined through the same workspace: captured twice, replayed in turn with eager calls of other sizes between; and on two
+    streams at once."""
+    m, k, n = 130, 20000, 131
+    assert zpm.zero_packed_workspace(zpm.ZERO_PACKED_LINEAR, m, k, n) >= 2 * m * 132 * 4
+    x, w, dy, z = random_packed(m, k, 3), random_packed(n, k, 4), whole_dy(30000, 80, F16, 2, 1), random_packed(30000, 96, 1)
+    assert zpm.zero_packed_workspace(zpm.ZERO_PACKED_WEIGHT_GRAD, 30000, 96, 80) > 2 * 96 * 80 * 4
+
+    def step(into):
+        into[0].copy_(x.zero_packed_linear(w, bias=w.scale, dtype=F32))
+        z.zero_packed_weight_grad(dy, out=into[1], bias_grad=into[2])
+        z.zero_packed_weight_grad(dy, out=into[1], bias_grad=into[2], accumulate=True)
+        return into
+
+    fresh = lambda: [torch.full(s, math.nan, device=DEV) for s in ((m, n), (80, 96), (80,))]
+    want = [(x.q.double() @ w.q.double().T).float() * x.scale[:, None] * w.scale + w.scale,
+            (2 * (dy.double().T @ values(z))).float(), (2 * dy.double().sum(0)).float()]
+    same = lambda got: all(torch.equal(a, b) for a, b in zip(got, want))
+    assert same(step(fresh()))
+    torch.cuda.synchronize()
+    outs, graphs = [fresh(), fresh()], []
+    for o in outs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(o)
+        graphs.append(g)
+    for turn in range(3):
+        for o, g in zip(outs, graphs):
+            for t in o:
+                t.fill_(5)
+            g.replay()
+            x[:70].zero_packed_linear(w)
+            z[:4000].zero_packed_weight_grad(dy[:4000], bias_grad=torch.empty(80, device=DEV))
+            torch.cuda.synchronize()
+            assert same(o), turn
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(step(fresh()))
+    torch.cuda.synchronize()
+    assert all(same(o) for o in got)
+
+
 def test_same_bits_every_time():
     """Whatever runs beside it, and in whatever order blocks end."""
     g = gen(3)
