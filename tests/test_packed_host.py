@@ -201,3 +201,12 @@ def test_binding_refuses():
                  (q, s), (q, None)):
         with pytest.raises(ValueError):
             ZeroPacked.of(*args)
+
+
+def test_lazily_negated_rows_refused():
+    """Their memory holds the opposite of their values."""
+    q, s = torch.ones(4, 32, dtype=torch.int8), torch.ones(4)
+    with pytest.raises(ValueError, match="negated"):
+        ZeroPacked.of(torch._neg_view(q), s)
+    with pytest.raises(ValueError, match="scale must be"):
+        ZeroPacked.of(q, torch._neg_view(s))

@@ -65,6 +65,8 @@ class ZeroPacked:
             raise ValueError("q and scale must be tensors")
         if q.dtype != torch.int8 or q.dim() != 2 or (q.shape[1] > 1 and q.stride(1) != 1):
             raise ValueError("q must be an int8 matrix whose rows are consecutive elements")
+        if q.is_neg():
+            raise ValueError("q: a lazily negated view; resolve_neg() it first")
         cols = q.shape[1] if cols is None else cols
         if scale.dtype != torch.float32 or scale.shape != q.shape[:1] or not scale.is_contiguous() or scale.is_neg():
             raise ValueError(f"scale must be {q.shape[0]} contiguous float32 values")
