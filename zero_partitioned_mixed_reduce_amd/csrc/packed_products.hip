@@ -662,6 +662,7 @@ __global__ void __launch_bounds__(WI* WJ * 64, 2) grad_kernel(GradArgs g, uint32
     Held& h = held[(K + 1) % 2];
     if constexpr (FEED == kDirect) {
       if (kInner || s + 3 < last) fill(inner, std::integral_constant<int, (K + 3) % 4>(), s + 3);
+      asm volatile("" ::: "memory");  // requested before load()'s: end_reading() below counts by that order
     }
 #pragma unroll
     for (int j = 0; j < TJ; ++j) fq[j] = fetch_q(k, j);
