@@ -61,6 +61,8 @@
  *     where a call says so; column slices of one matrix are told apart by their
  *     pitch.
  *   - Matrices without rows or columns are fine; their addresses may be NULL.
+ *   - A product's result of 2^22 tiles or more is refused: tiles of 256 x 256, in a
+ *     linear layer of up to 64 tokens of 16 columns.
  */
 #ifndef ZERO_PACKED_H
 #define ZERO_PACKED_H

@@ -1,5 +1,5 @@
 // C ABI of the packed-row operators.  Host side: argument checks and kernel launches.  The
-// arithmetic is in packed_rows.hip and packed_products.hip.
+// arithmetic is in packed_rows.hip, packed_act.hip and packed_products.hip.
 #include <hip/hip_runtime.h>
 
 #include <exception>

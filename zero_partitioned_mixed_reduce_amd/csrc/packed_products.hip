@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) linear_kernel(LinearArgs a, ui
     at[u] = (uint32_t)(r < edge ? r : edge) * (uint32_t)(u < LX ? a.x.pitch : a.w.pitch) + chunk * 16u;
   }
   const auto fill = [&](int step) __attribute__((always_inline)) {
-    // chunks past a row's end read its last one; fetch() leaves them out
+    // chunks past a row's end read its last one; run() leaves them out
     const int most = chunks - 1 - step * 4;
     const int back = chunk > most ? (most - chunk) * 16 : 0;
     char* to = lds[(unsigned)step % kStages];
@@ -412,7 +412,7 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
 // A block makes a tile of BI x BJ results with WI x WJ waves: 256 x 256 with eight, or 128 x 256 where a
 // comes through registers, and 128 x 128 with four for small results.  The weight gradient of
 // 8192 x 4096 x 11008 takes 653 us, 1.13e15 FLOP/s (1.20e15 at 8192 cubed), the input gradient of that
-// size 587, 1.26e15, whose a needs no transposing reads; in two terms 2047 x 4096 x 4096 takes 139 us,
+// size 587, 1.26e15, whose a needs no transposing reads; in two terms 2047 x 4096 x 4096 takes 140 us,
 // 0.99e15 of both.  Bound by the matrix cores and, a third of the instructions beside theirs, the
 // conversion of q: each block converts its 32 x BJ values of a step once, two 16-byte loads ahead.
 // (Conversion spread between the products by scheduling groups: 923 for 857 us then.)
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(WI* WJ * 64, 2) grad_kernel(GradArgs g, uint32
     const int64_t s0 = (int64_t)step * S;
     const char* base = (const char*)g.a.p + (TRANS ? s0 * g.a.pitch + i0 : i0 * g.a.pitch + s0) * 2;
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, 0xFFFFFFFFu, 0x00020000);
-    // past the end of s the last row or chunk is read; multiply() leaves it out
+    // past the end of s the last row or chunk is read; run() leaves it out
     const int over = (int)(s0 + S - g.nc);
     char* to = a_place(k);
 #pragma unroll
@@ -868,6 +868,9 @@ ProductPlan plan_linear(int64_t m, int64_t k, int64_t n) {
     few.ws_bytes = 0;
     return few;
   }
+  // 256 large tiles fill the chip.  k = 1600 and 8192 in bf16: 128 tiles' worth of results in large tiles 28
+  // and 86 us, in small ones 24 and 83; 256 34 and 115, 45 and 160; 272 54 and 188, 52 and 191.  (From 144 to
+  // 255 the large ones would be ahead too: 224 31 and 104, 41 and 150.)
   const ProductPlan p = plan_product(m, n, up(k, kStepK), 256, 256, kBigStep);
   return p.tiles_i * p.tiles_j >= 256 ? p : plan_product(m, n, up(k, kStepK), 128, 128, kLinearStep);
 }
@@ -902,6 +905,10 @@ static bool direct(const GradArgs& g, bool trans) {
   return g.a.dtype == ZERO_BF16 && g.q.rule == ZERO_SCALE_POW2 && (uintptr_t)g.a.p % 16 == 0 && g.a.pitch % 8 == 0 &&
          along % 8 == 0 && along > 0 && g.a.pitch <= (int64_t)1 << 22;
 }
+// Large tiles from half of what the chip takes at once.  Weight gradients over 1600 and 8192 rows: 64 large
+// tiles 59 and 111 us, as many results in small tiles 43 and 105; 128 62 and 153, 46 and 159; 256 73 and 246,
+// 80 and 308; 512 135 and 477, 143 and 588.  (From 257 to about 320 tiles the second round of large ones is
+// nearly empty, and the small ones would be ahead: 272 120 and 442, 90 and 349.)
 ProductPlan plan_grad(int64_t ni, int64_t nj, int64_t nc) {
   const ProductPlan p = plan_product(ni, nj, up(nc, kStepS), 256, 256, kBigStep);
   return p.tiles_i * p.tiles_j >= 128 ? p : plan_product(ni, nj, up(nc, kStepS), 128, 128, kGradStep);

@@ -5,7 +5,8 @@
 // takes a row of up to 2048 elements, four rows to a block, and a block of 256 to 1024 threads one
 // of up to 32 elements a thread.  Rows beyond 32768 elements are read twice, the second time
 // mostly from the L2 cache.  16384 x 11008 in bf16: packed in 86 us (6.3 TB/s; 110 with ordinary
-// loads), read back in 108 (5.0); a copy reaches 6.4.
+// loads), by ZERO_SCALE_MAX in 105 to 112 (5.0), whose rounding takes more instructions, read back in
+// 108 (5.0); a copy reaches 6.4.
 #include "packed_rows.h"
 
 namespace zs {
