@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import zero_partitioned_mixed_reduce_amd as zpm
+from zero_partitioned_mixed_reduce_amd.packed import matrix
 
 pytestmark = pytest.mark.gpu
 
@@ -163,6 +164,28 @@ def test_rows_with_infinities(cols, bad):
         assert (p.zero_packed_read()[4].view(torch.int16) == 0x7FC0).all()
 
 
+@pytest.mark.parametrize("rows, cols", [((1 << 22) + 9, 24), ((1 << 20) + 3, 2056), ((1 << 20) + 3, 2051)])
+def test_more_rows_than_a_launch_has_blocks(rows, cols):
+    """Blocks go on to further rows, where a row's threads are a wave and where they are a block."""
+    x = torch.randn(rows, cols, generator=gen(cols), device=DEV, dtype=BF16)
+    x[-1] = 0
+    x[-2, 3] = math.inf
+    p = zpm.ZeroPacked(rows, cols).zero_packed_write(x)
+    blocks = 1 << 20
+    at = torch.cat([torch.arange(a, a + 16, device=DEV) for a in (0, blocks - 8, rows // 2, rows - 16)])
+    at = at[at < rows]
+    q, s = packed_of(x[at], POW2)
+    assert same_bits(p.scale[at], s) and torch.equal(p.q[at], q)
+    y = p.zero_packed_read()
+    assert y[-2].isnan().all() and not y[-1].any() and y[:-2].isfinite().all()
+    assert torch.equal(y[at].nan_to_num(), (p.q[at].float() * p.scale[at, None]).to(BF16).nan_to_num())
+    # the packed rows of the whole matrix agree with those of pieces that one launch covers
+    del y
+    a = rows - (1 << 18)
+    r = zpm.ZeroPacked(1 << 18, cols).zero_packed_write(x[a:])
+    assert torch.equal(r._q, p._q[a:]) and same_bits(r.scale, p.scale[a:])
+
+
 def test_no_rows_and_no_columns():
     for rows, cols in ((0, 40), (7, 0), (0, 0)):
         p = zpm.ZeroPacked(rows, cols)
@@ -249,6 +272,29 @@ def test_linear_far_offsets():
     y = x.zero_packed_linear(w)
     for r in (0, 42949, 42950, m - 1):                 # around element 2^31
         assert torch.equal(y[r:r + 1], linear_expected(x[r:r + 1], w, None, BF16))
+
+
+@pytest.mark.parametrize("m", [1, 16, 17, 33, 64])
+@pytest.mark.parametrize("k, n", [(33, 2050), (1100, 2048), (4096, 8191), (700, 8192), (1024, 9001)])
+def test_linear_of_few_tokens_into_many_channels(m, k, n):
+    x, w = random_packed(m, k, 1), random_packed(n, k, 2, MAX, torch.rand(n, generator=gen(3), device=DEV) + 0.01)
+    assert same_bits(x.zero_packed_linear(w, bias=w.scale, dtype=F32), linear_expected(x, w, w.scale, F32))
+    y, big = strided(torch.zeros(m, n, dtype=BF16, device=DEV), 7, 1)
+    x.zero_packed_linear(w, out=y)
+    assert torch.equal(y, linear_expected(x, w, None, BF16)) and around(y, big, 1).isnan().all()
+
+
+@pytest.mark.parametrize("m, n", [(3, 17), (64, 40), (130, 129)])
+def test_linear_of_the_largest_sums(m, n):
+    """131056 products of the largest bytes there are, of one sign and of both: sums next to 2^31."""
+    k = 131056
+    x, w = random_packed(m, k, 1), random_packed(n, k, 2)
+    x._q.fill_(-128), w._q.fill_(-128)
+    w._q[n // 2:].fill_(127)
+    w._q[:, k:], x._q[:, k:] = 0, 0
+    y = x.zero_packed_linear(w, dtype=F32)
+    assert same_bits(y, linear_expected(x, w, None, F32))
+    assert (y[:, 0] == (2.0 ** 31 - 2.0 ** 18) * x.scale * w.scale[0]).all()
 
 
 # --- gradients
@@ -520,6 +566,45 @@ def test_gradients_of_nothing():
     assert (db == 5).all()
 
 
+def test_products_of_the_largest_pitches():
+    """Rows as far apart as the calls allow: tiles' rows then lie up to 2^31 bytes apart."""
+    m, k, n, far = 300, 72, 40, 1 << 22
+
+    def apart(p):
+        wide = torch.empty(p.rows, far, dtype=torch.int8, device=DEV)
+        wide[:, :p._q.shape[1]] = p._q
+        return zpm.ZeroPacked.of(wide, p.scale, p.cols, p.rule)
+    x, w = random_packed(m, k, 1), random_packed(n, k, 2)
+    xf = apart(x)
+    assert torch.equal(xf.zero_packed_linear(w), linear_expected(x, w, None, BF16))
+    assert torch.equal(w.zero_packed_linear(xf), linear_expected(w, x, None, BF16))
+    wf = apart(random_packed(300, k, 3))
+    assert torch.equal(xf.zero_packed_linear(wf), linear_expected(x, wf, None, BF16))
+    del wf
+    assert torch.equal(xf.zero_packed_read(), x.zero_packed_read())
+    dy, dz = whole_dy(m, n, BF16, 5), whole_dy(n, m, BF16, 6)
+    want, want_x = (dy.double().T @ values(x)).float(), (dz.double() @ values(x)).float()
+    for dtype in (BF16, F16):
+        assert torch.equal(xf.zero_packed_weight_grad(dy.to(dtype)), want)
+        assert torch.equal(xf.zero_packed_input_grad(dz.to(dtype), dtype=F32), want_x)
+    del xf
+    # dy's rows: the farthest that go straight into LDS, and beyond
+    for pitch in (far, far + 8):
+        wide = torch.empty(m, pitch, dtype=BF16, device=DEV)
+        wide[:, :n] = dy
+        assert torch.equal(x.zero_packed_weight_grad(wide[:, :n]), want)
+        tall = torch.empty(m, pitch, dtype=BF16, device=DEV)
+        tall[:, :n] = dy
+        assert torch.equal(w.zero_packed_input_grad(tall[:, :n], dtype=F32), (dy.double() @ values(w)).float())
+        del wide, tall
+    wide = torch.empty(5, 1 << 30, dtype=BF16, device=DEV)
+    wide[:, :n] = dy[:5]
+    assert torch.equal(x[:5].zero_packed_weight_grad(wide[:, :n]), (dy[:5].double().T @ values(x[:5])).float())
+    out = wide[:, 64:64 + k]
+    w.zero_packed_input_grad(dy[:5], out=out)
+    assert torch.equal(out, (dy[:5].double() @ values(w)).to(BF16))
+
+
 def test_gradient_far_offsets():
     """dy of more than 2^31 elements (both orders), and a weight gradient of more than 2^31 bytes."""
     m, n, k = 65600, 32800, 40
@@ -597,6 +682,43 @@ def test_act(rows, n, kind, gated):
         alone = zpm.ZeroPacked(rows, n, rule)
         assert zpm.ZeroPacked(*x.shape).zero_packed_act(x, kind, gated, packed=alone) is alone
         assert torch.equal(alone._q, yp._q)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("rows, n", [(5, 33), (3, 1031), (2, 4100), (2, 20001), (2, 20008)])
+def test_act_results_one_by_one(rows, n, gated):
+    """Each result by itself, by the C names, is the one of the call that asks for all; the packed two by rules of their own."""
+    stream = torch.cuda.current_stream().cuda_stream
+    x = (3 * torch.randn(rows, 2 * n if gated else n, generator=gen(n), device=DEV)).to(BF16)
+    new = lambda cols, rule: zpm.ZeroPacked(rows, cols, rule)
+    xp, yp, y = new(x.shape[1], MAX), new(n, POW2), torch.empty(rows, n, device=DEV)
+    for t in (xp, yp):
+        t._q.fill_(99)
+    zpm.zero_packed_act(SILU, gated, matrix(x, "x"), xp._desc, matrix(y, "y"), yp._desc, stream)
+    for p, want in ((xp, packed_of(x, MAX)), (yp, packed_of(y, POW2))):
+        assert torch.equal(p.q, want[0]) and same_bits(p.scale, want[1]) and not p._q[:, p.cols:].any()
+    y1, xp1, yp1 = torch.empty_like(y), new(x.shape[1], MAX), new(n, POW2)
+    zpm.zero_packed_act(SILU, gated, matrix(x, "x"), None, matrix(y1, "y"), None, stream)
+    zpm.zero_packed_act(SILU, gated, matrix(x, "x"), xp1._desc, None, None, stream)
+    zpm.zero_packed_act(SILU, gated, matrix(x, "x"), None, None, yp1._desc, stream)
+    assert torch.equal(y1, y)
+    assert torch.equal(xp1.q, xp.q) and torch.equal(xp1.scale, xp.scale) and torch.equal(yp1.q, yp.q) and torch.equal(yp1.scale, yp.scale)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_act_of_more_rows_than_a_launch_has_blocks(gated):
+    rows, n = (1 << 20) + 3, 1032
+    x = torch.randn(rows, 2 * n if gated else n, generator=gen(n), device=DEV, dtype=BF16)
+    xp, yp = zpm.ZeroPacked(*x.shape), zpm.ZeroPacked(rows, n)
+    y = xp.zero_packed_act(x, GELU, gated, packed=yp, dtype=BF16)
+    dx = xp.zero_packed_act_grad(y, GELU, gated)
+    for a in (0, rows - 128):
+        b = slice(a, a + 128)
+        xq, yq = zpm.ZeroPacked(128, x.shape[1]), zpm.ZeroPacked(128, n)
+        assert torch.equal(xq.zero_packed_act(x[b], GELU, gated, packed=yq, dtype=BF16), y[b])
+        for got, want in ((xp[b], xq), (yp[b], yq)):
+            assert torch.equal(got.q, want.q) and torch.equal(got.scale, want.scale)
+        assert torch.equal(xq.zero_packed_act_grad(y[b], GELU, gated), dx[b])
 
 
 @pytest.mark.parametrize("gated", [False, True])
